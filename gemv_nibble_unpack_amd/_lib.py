@@ -20,11 +20,17 @@ W4_LAYOUT_W4A8, W4_LAYOUT_W4A16, W4_LAYOUT_W2A8, W4_LAYOUT_W8A8 = 0, 1, 2, 3
 W4_OP_W4A8, W4_OP_W4A16, W4_OP_W2A8, W4_OP_W2A16, W4_OP_W8A8, W4_OP_F8F8 = 0, 1, 2, 3, 4, 5
 W4_GROUP_SIZE = 128
 W4_MAX_K = 131056
+# mirror include/gemv_nibble_unpack_layer.h
+W4_Q_I8, W4_Q_F8 = 0, 1
+W4_ROPE_HALF, W4_ROPE_INTERLEAVED = 0, 1
+W4_MAX_HEAD_DIM = 256
+W4_ATTN_WORKSPACE_MAX = 64 * 1024 * 1024
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _i64 = ctypes.c_int64
+_f = ctypes.c_float
 
 # name -> (restype, argtypes); the order follows the header
 SIGNATURES = {
@@ -64,6 +70,17 @@ SIGNATURES = {
     "w4_graph_destroy": (_i, [_p]),
 }
 
+# the decoder-layer operators; the order follows their header
+LAYER_SIGNATURES = {
+    "add_rmsnorm_q8": (_i, [_p, _p, _p, _i, _i, _i, _f, _i, _p, _p, _p, _p]),
+    "kv8_padded_dim": (_i, [_i]),
+    "rope_append_kv8": (_i, [_p, _p, _p, _i, _i64, _i64, _i64, _p, _i, _i, _i, _p, _p, _p,
+                             _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p]),
+    "paged_attn_kv8_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "paged_attn_kv8": (_i, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i,
+                            _i, _i, _i, _f, _p, _p, _p, _sz, _p]),
+}
+
 _LIB = None
 
 
@@ -81,7 +98,7 @@ def load():
             f"{LIB_PATH} not found: build it first (python -c 'import __graft_entry__ as g; g.build()')"
             " -- this package has no CPU fallback")
     lib = ctypes.CDLL(LIB_PATH)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in {**SIGNATURES, **LAYER_SIGNATURES}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

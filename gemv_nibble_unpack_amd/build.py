@@ -15,6 +15,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["quant.hip", "prepack.hip", "matmul.hip", "gemm_launch.hip", "probe.hip", "noalloc.hip",
            "graph.hip", "gemm16.hip"]
+# the decoder-layer operators, beside csrc: the traffic records of the matmul
+# kernels carry a hash over csrc, which these sources do not change
+LAYER_CSRC = os.path.join(HERE, "csrc_layer")
+LAYER_SOURCES = ["norm.hip", "append.hip", "attn.hip"]
 OUT = os.path.join(HERE, "libgemv_nibble_unpack.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 ARCH = os.environ.get("W4_OFFLOAD_ARCH", "gfx950")
@@ -57,10 +61,11 @@ def build(verbose=True, jobs=None):
     code; no device function is called across units."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
-    objs = [os.path.join(OBJ_DIR, os.path.splitext(s)[0] + ".o") for s in SOURCES]
+    srcs = ([os.path.join(CSRC, s) for s in SOURCES] +
+            [os.path.join(LAYER_CSRC, s) for s in LAYER_SOURCES])
+    objs = [os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(s))[0] + ".o") for s in srcs]
     cflags = [f for f in FLAGS if f != "-shared"]
-    cmds = [[hipcc(), *cflags, *inc, "-c", os.path.join(CSRC, s), "-o", o]
-            for s, o in zip(SOURCES, objs)]
+    cmds = [[hipcc(), *cflags, *inc, "-c", s, "-o", o] for s, o in zip(srcs, objs)]
     jobs = jobs or min(len(cmds), max(1, (os.cpu_count() or 1)))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         for f in [ex.submit(_run, c, verbose) for c in cmds]:

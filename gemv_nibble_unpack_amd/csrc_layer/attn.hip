@@ -1,0 +1,494 @@
+// Attention of one or a few new tokens over the paged 8-bit cache.
+//
+// The query rows of a (sequence, kv head) are its new tokens times the query
+// heads that share the kv head, token-major; a block takes 16 * QT of them and
+// one chunk of the cached tokens. Each of its four waves takes every fourth
+// step of 64 tokens, with a running maximum, sum and output of its own:
+//
+//   S^T = K q^T    v_mfma_f32_16x16x32_f16, rows = tokens, columns = query rows
+//   w   = 2^(S a - m)           float32; a = k_scale * sm_scale * log2 e
+//   O^T += V^T w^T              the same instruction, rows = dims
+//
+// Token order inside a step is chosen so that nothing moves between lanes: the
+// wave's four 16-lane rows g own the tokens 16g .. 16g+15. Row i of the K
+// operand of tile t is token 16 (i >> 2) + 4 t + (i & 3); the product leaves
+// lane (column c, row g) with tokens 16 g + 4 t + 0..3, which over two tiles are
+// the 8 consecutive tokens that the second product's k slots of that lane
+// take, and the V operand reads them as 8 consecutive bytes of the transposed
+// value page. 16 tokens lie in one page, so a lane needs one key scale and one
+// value scale per step. The codes are widened to fp16 in registers (exact).
+//
+// Value scales: with r the largest value scale met so far, w is multiplied by
+// v_scale / r <= 1 before its rounding to fp16 and O is kept in units of r
+// (rescaled together with the running maximum), so weights keep fp16's
+// relative precision at any magnitude of the values. The factor 2^10 on w
+// moves small weights out of fp16's subnormals.
+//
+// Chunks: a sequence's chunks are joined by the block that arrives last
+// (agent-scope stores and loads, one arrival counter per row tile, left zero).
+// Bound: the bytes of the codes (2 per cached token, head and dim).
+
+#include "attn.hpp"
+
+namespace w4 {
+
+constexpr float P_UP = 1024.0f;
+constexpr float REF_MIN = 0x1p-100f;
+
+template <int DP, int Q, int QT>
+struct AttnFew {
+  static constexpr int ROWS = 16 * QT;
+  static constexpr int KH = DP / 64;                // 64-dim halves of a K row
+  static constexpr bool KR = DP % 64 != 0;          // and a rest of 32 dims
+  static constexpr int KS = DP / 32;                // k steps of the first product
+  static constexpr int DT = DP / 16;                // 16-dim tiles of the second
+  static constexpr int OROW = DP + 4;               // staged floats per row
+  static constexpr int LDS = 4 * ROWS * OROW * 4 + 4 * ROWS * 2 * 4 + 16 + 16;
+};
+
+template <int DP>
+struct KVRegs {
+  u4 k[4][DP / 64 ? DP / 64 : 1];
+  u2 kr[4];
+  u4 v[DP / 16];
+  float ks, vs;
+};
+
+template <int DP, int Q, int QT>
+__global__ __launch_bounds__(256) void k_attn_few(const AttnParams p) {
+  using C = AttnFew<DP, Q, QT>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  float* so = reinterpret_cast<float*>(smem);                       // [4][ROWS][OROW]
+  float* sml = so + 4 * C::ROWS * C::OROW;                          // [4][ROWS][2]
+  float* sref = sml + 4 * C::ROWS * 2;                              // [4]
+  unsigned* slast = reinterpret_cast<unsigned*>(sref + 4);
+
+  int t = blockIdx.x;
+  const int h = t % p.kv_heads;
+  t /= p.kv_heads;
+  const int tile = t % p.tiles;
+  t /= p.tiles;
+  const int b = t % p.batch;
+  const int split = t / p.batch;
+  int row0, n, len;
+  bool fits;
+  if (!attn_span(p, b, row0, n, len, fits)) return;
+  const int rows = min(n, p.max_q) * p.group;
+  const int r0 = tile * C::ROWS;
+  if (r0 >= rows) return;
+  const int nr = min(rows - r0, C::ROWS);           // rows of this tile
+  const int first = len - n;                        // position of new token 0
+  // cached tokens that the tile's last row sees
+  const int seen = fits ? max(0, first + (r0 + nr - 1) / p.group + 1) : 0;
+  const int parts = max(1, (seen + p.chunk - 1) / p.chunk);
+  if (split >= parts) return;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int P = 1 << p.page_shift;
+
+  // ---- this lane's query rows (columns c of QT operands) -------------------
+  h8 qf[QT][C::KS];
+  int lim[QT];                                      // tokens that the row sees
+#pragma unroll
+  for (int u = 0; u < QT; ++u) {
+    const int r = r0 + 16 * u + c;
+    const bool in = r < rows;
+    const int rc = in ? r : r0;
+    const int tok = rc / p.group, hh = h * p.group + (rc - tok * p.group);
+    lim[u] = in && fits ? first + tok + 1 : 0;
+    const uint16_t* q = p.q + (int64_t)(row0 + tok) * p.q_stride + (int64_t)hh * p.dim;
+    auto quad = [&](int d) {                         // dims past the head are zero
+      return d < p.dim ? *reinterpret_cast<const u2*>(q + d) : u2{0u, 0u};
+    };
+    auto oct = [&](int d) {
+      const u2 a = quad(d), b2 = quad(d + 4);
+      return __builtin_bit_cast(h8, u4{a[0], a[1], b2[0], b2[1]});
+    };
+#pragma unroll
+    for (int s = 0; s < C::KH; ++s) {
+      qf[u][2 * s] = oct(64 * s + 16 * g);
+      qf[u][2 * s + 1] = oct(64 * s + 16 * g + 8);
+    }
+    if constexpr (C::KR) qf[u][C::KS - 1] = oct(64 * C::KH + 8 * g);
+  }
+
+  const int32_t* tab = p.table + (size_t)b * p.cols;
+  const int c0 = split * p.chunk;
+  const int c1 = min(seen, c0 + p.chunk);
+  const int last16 = (max(seen, 1) - 1) & ~15;      // start of the last group with a token
+  const size_t kpage = (size_t)p.kv_heads << p.page_shift;   // rows per page
+
+  // Step at token t: group of tokens of K operand row c and of row g
+  auto load = [&](int t0, KVRegs<DP>& r) {
+    const int tk = min(t0 + 16 * (c >> 2), last16), tv = min(t0 + 16 * g, last16);
+    int ik = tab[tk >> p.page_shift], iv = tab[tv >> p.page_shift];
+    const bool okv = iv >= 0 && iv < p.pages;
+    ik = ik >= 0 && ik < p.pages ? ik : 0;
+    iv = okv ? iv : 0;
+    const size_t sv = (size_t)iv * p.kv_heads + h;
+    r.ks = okv ? p.ks[sv] : __uint_as_float(0x7FC00000u);
+    r.vs = p.vs[sv];
+    const uint8_t* kp = p.kc + ((size_t)ik * kpage + ((size_t)h << p.page_shift) +
+                                (tk & (P - 1)) + (c & 3)) * DP;
+    const uint8_t* vp = p.vc + (((size_t)iv * p.kv_heads + h) * DP + c) * P + (tv & (P - 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int s = 0; s < C::KH; ++s)
+        r.k[i][s] = *reinterpret_cast<const u4*>(kp + 4 * i * DP + 64 * s + 16 * g);
+      if constexpr (C::KR)
+        r.kr[i] = *reinterpret_cast<const u2*>(kp + 4 * i * DP + 64 * C::KH + 8 * g);
+    }
+#pragma unroll
+    for (int d = 0; d < C::DT; ++d) r.v[d] = *reinterpret_cast<const u4*>(vp + (size_t)16 * d * P);
+  };
+
+  f4 o[QT][C::DT];
+  float m[QT], l[QT];
+  float ref = REF_MIN;
+#pragma unroll
+  for (int u = 0; u < QT; ++u) {
+    m[u] = -__builtin_inff();
+    l[u] = 0.f;
+#pragma unroll
+    for (int d = 0; d < C::DT; ++d) o[u][d] = f4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  auto step = [&](int t0, KVRegs<DP>& r) {
+    f4 s[QT][4];
+#pragma unroll
+    for (int u = 0; u < QT; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[u][i] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int x = 0; x < C::KH; ++x) {
+        const h8 a0 = widen8<Q>(r.k[i][x][0], r.k[i][x][1]);
+        const h8 a1 = widen8<Q>(r.k[i][x][2], r.k[i][x][3]);
+#pragma unroll
+        for (int u = 0; u < QT; ++u) {
+          s[u][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, qf[u][2 * x], s[u][i], 0, 0, 0);
+          s[u][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, qf[u][2 * x + 1], s[u][i], 0, 0, 0);
+        }
+      }
+      if constexpr (C::KR) {
+        const h8 a = widen8<Q>(r.kr[i][0], r.kr[i][1]);
+#pragma unroll
+        for (int u = 0; u < QT; ++u)
+          s[u][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[u][C::KS - 1], s[u][i], 0, 0, 0);
+      }
+    }
+    const int tg = t0 + 16 * g;                     // this lane's 16 tokens
+    const float a = r.ks * p.scale_log2;
+    // a lane without a token in reach may hold any scale: it counts as none
+    const float vs = tg < c1 ? r.vs : 0.f;
+    const float nref = fmaxf(ref, rows_max(vs));
+    const float shrink = ref / nref;
+    const float pv = vs / nref * P_UP;
+    ref = nref;
+    h8 w[QT][2];
+#pragma unroll
+    for (int u = 0; u < QT; ++u) {
+      const int left = min(lim[u], c1) - tg;        // of the 16, the first `left` count
+      // a page that the row does not see may have any scale, NaN among them
+      const float pvu = left > 0 ? pv : 0.f;
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = s[u][i][e] * a;
+          s[u][i][e] = 4 * i + e < left ? x : -__builtin_inff();
+          mx = fmaxf(mx, s[u][i][e]);
+        }
+      const float nm = fmaxf(m[u], rows_max(mx));
+      const float base = nm == -__builtin_inff() ? 0.f : nm;
+      const float alpha = __builtin_amdgcn_exp2f(m[u] - base);
+      m[u] = nm;
+      float sum = 0.f;
+      h8 hw[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = __builtin_amdgcn_exp2f(s[u][i][e] - base);
+          sum += x;
+          hw[i >> 1][4 * (i & 1) + e] = (_Float16)(x * pvu);
+        }
+      l[u] = l[u] * alpha + sum;
+      w[u][0] = hw[0];
+      w[u][1] = hw[1];
+      const float f = alpha * shrink;
+#pragma unroll
+      for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[u][d][e] *= f;
+    }
+    // codes past the length may be E4M3 NaNs: 0 * NaN would reach the sums
+    if (Q == W4_Q_F8 && t0 + 64 > c1) {
+      const int left = min(max(c1 - tg, 0), 16);
+#pragma unroll
+      for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = min(max(left - 4 * e, 0), 4);
+          r.v[d][e] &= k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < C::DT; ++d) {
+      const h8 v0 = widen8<Q>(r.v[d][0], r.v[d][1]);
+      const h8 v1 = widen8<Q>(r.v[d][2], r.v[d][3]);
+#pragma unroll
+      for (int u = 0; u < QT; ++u) {
+        o[u][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w[u][0], o[u][d], 0, 0, 0);
+        o[u][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w[u][1], o[u][d], 0, 0, 0);
+      }
+    }
+  };
+
+  {
+    KVRegs<DP> r;
+    for (int t0 = c0 + 64 * wave; t0 < c1; t0 += 256) {
+      load(t0, r);
+      step(t0, r);
+    }
+  }
+
+  // ---- the four waves' results to LDS ---------------------------------------
+#pragma unroll
+  for (int u = 0; u < QT; ++u) {
+    const float lt = rows_sum(l[u]);
+    const int r = 16 * u + c;
+    if (g == 0) {
+      sml[(wave * C::ROWS + r) * 2] = m[u];
+      sml[(wave * C::ROWS + r) * 2 + 1] = lt;
+    }
+#pragma unroll
+    for (int d = 0; d < C::DT; ++d)
+      *reinterpret_cast<f4*>(so + (wave * C::ROWS + r) * C::OROW + 16 * d + 4 * g) = o[u][d];
+  }
+  if (lane == 0) sref[wave] = ref;
+  __syncthreads();
+
+  // Row r's result over the four waves: M, L and, for 4 dims, O in absolute
+  // units (sum of 2^(s - M) v)
+  auto waves_ml = [&](int r, float (&f)[4], float& M, float& L) {
+    M = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) M = fmaxf(M, sml[(i * C::ROWS + r) * 2]);
+    const float base = M == -__builtin_inff() ? 0.f : M;
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e = __builtin_amdgcn_exp2f(sml[(i * C::ROWS + r) * 2] - base);
+      L += e * sml[(i * C::ROWS + r) * 2 + 1];
+      f[i] = e * sref[i] * (1.0f / P_UP);
+    }
+  };
+  auto waves_o = [&](int r, int d, const float (&f)[4]) {
+    f4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f4 x = *reinterpret_cast<const f4*>(so + (i * C::ROWS + r) * C::OROW + d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += f[i] * x[e];
+    }
+    return s;
+  };
+  auto finish = [&](int r, int d, float M, float L, f4 s) {
+    const int rr = r0 + r, tok = rr / p.group, hh = h * p.group + (rr - tok * p.group);
+    const size_t at = (size_t)(row0 + tok) * p.q_heads + hh;
+    const float nan = __uint_as_float(0x7FC00000u);
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
+    h4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = (_Float16)(fits ? s[e] * inv : nan);
+    if (d < p.dim) *reinterpret_cast<u2*>(p.out + at * p.dim + d) = __builtin_bit_cast(u2, y);
+    if (p.lse && d == 0) {
+      const float v = M + __builtin_amdgcn_logf(L);          // log2 units
+      p.lse[at] = !fits ? nan : L == 0.f ? -__builtin_inff() : v * 0.69314718055994531f;
+    }
+  };
+  constexpr int NV = DP / 4;
+  if (parts == 1) {
+    for (int i = tid; i < nr * NV; i += 256) {
+      const int r = i / NV, d = 4 * (i % NV);
+      float f[4], M, L;
+      waves_ml(r, f, M, L);
+      finish(r, d, M, L, waves_o(r, d, f));
+    }
+    return;
+  }
+
+  // ---- split over chunks: store the part, the last block joins --------------
+  const size_t unit = ((size_t)b * p.kv_heads + h) * p.tiles + tile;
+  uint32_t* po = reinterpret_cast<uint32_t*>(p.part) +
+                 unit * p.splits * (size_t)(C::ROWS * (DP + 2));
+  const size_t pstride = (size_t)C::ROWS * (DP + 2);          // one part: O rows, then (M, L)
+  for (int i = tid; i < nr * NV; i += 256) {
+    const int r = i / NV, d = 4 * (i % NV);
+    float f[4], M, L;
+    waves_ml(r, f, M, L);
+    const f4 s = waves_o(r, d, f);
+    uint32_t* q = po + split * pstride;
+    dev_store2(q + r * DP + d, __float_as_uint(s[0]), __float_as_uint(s[1]));
+    dev_store2(q + r * DP + d + 2, __float_as_uint(s[2]), __float_as_uint(s[3]));
+    if (d == 0) dev_store2(q + C::ROWS * DP + 2 * r, __float_as_uint(M), __float_as_uint(L));
+  }
+  stores_done();
+  __syncthreads();
+  if (tid == 0) *slast = dev_arrive(p.counters + unit) == (unsigned)(parts - 1);
+  __syncthreads();
+  if (!*slast) return;
+  if (tid == 0) dev_store(p.counters + unit, 0u);
+  for (int i = tid; i < nr * NV; i += 256) {
+    const int r = i / NV, d = 4 * (i % NV);
+    float M = -__builtin_inff(), L = 0.f;
+    f4 s = {0.f, 0.f, 0.f, 0.f};
+    // parts four at a time, their loads issued together
+    for (int z = 0; z < parts; z += 4) {
+      uint64_t ml[4], a[4], e2[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t* q = po + min(z + k, parts - 1) * pstride;
+        ml[k] = dev_load2(q + C::ROWS * DP + 2 * r);
+        a[k] = dev_load2(q + r * DP + d);
+        e2[k] = dev_load2(q + r * DP + d + 2);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (z + k >= parts) break;
+        const float Mk = __uint_as_float((uint32_t)ml[k]), Lk = __uint_as_float(ml[k] >> 32);
+        const float nm = fmaxf(M, Mk);
+        const float base = nm == -__builtin_inff() ? 0.f : nm;
+        const float fo = __builtin_amdgcn_exp2f(M - base), fn = __builtin_amdgcn_exp2f(Mk - base);
+        M = nm;
+        L = L * fo + Lk * fn;
+        s[0] = s[0] * fo + __uint_as_float((uint32_t)a[k]) * fn;
+        s[1] = s[1] * fo + __uint_as_float((uint32_t)(a[k] >> 32)) * fn;
+        s[2] = s[2] * fo + __uint_as_float((uint32_t)e2[k]) * fn;
+        s[3] = s[3] * fo + __uint_as_float((uint32_t)(e2[k] >> 32)) * fn;
+      }
+    }
+    finish(r, d, M, L, s);
+  }
+}
+
+// The launch for these sizes: rows per tile, tiles, chunk and splits, and the
+// workspace they need.
+struct AttnPlan {
+  int qt, tiles, chunk, splits;
+  int64_t units;
+  size_t ws;
+};
+
+inline AttnPlan attn_plan(int batch, int max_q, int max_kv, int group, int kv_heads, int dp) {
+  AttnPlan a{};
+  const int64_t rows = (int64_t)max_q * group;
+  a.qt = rows > 16 ? 2 : 1;
+  a.tiles = (int)((rows + 16 * a.qt - 1) / (16 * a.qt));
+  a.units = (int64_t)batch * kv_heads * a.tiles;
+  int64_t splits = 1;
+  if (a.units <= WS_COUNTER_SLOTS)
+    splits = max((int64_t)1, min((int64_t)(max_kv + 255) / 256, 1024 / a.units));
+  a.chunk = (int)(((max_kv + splits - 1) / splits + 255) / 256 * 256);
+  a.splits = max(1, (max_kv + a.chunk - 1) / a.chunk);
+  a.ws = a.splits == 1 ? 0
+                       : WS_COUNTERS + (size_t)a.units * a.splits * 16 * a.qt * (dp + 2) * 4;
+  return a;
+}
+
+template <int DP, int Q>
+int launch_attn(const AttnParams& p, const AttnPlan& a, hipStream_t stream) {
+  const int64_t blocks = a.units * a.splits;
+  if (blocks > 0x7fffff) return W4_ERR_SHAPE;
+#define W4_AT(QT)                                                                       \
+  do {                                                                                  \
+    constexpr int lds = AttnFew<DP, Q, QT>::LDS;                                        \
+    allow_smem((const void*)k_attn_few<DP, Q, QT>, lds);                                \
+    hipLaunchKernelGGL((k_attn_few<DP, Q, QT>), dim3((unsigned)blocks), dim3(256), lds, \
+                       stream, p);                                                      \
+  } while (0)
+  if (a.qt == 1) W4_AT(1);
+  else W4_AT(2);
+#undef W4_AT
+  return launch_status();
+}
+
+}  // namespace w4
+
+using namespace w4;
+
+static bool attn_sizes_ok(int batch, int tokens, int max_q, int max_kv, int q_heads, int kv_heads,
+                          int head_dim) {
+  return batch >= 0 && tokens >= 0 && max_q >= 0 && max_kv >= 0 && max_kv <= (1 << 30) &&
+         kv_heads >= 1 && q_heads >= 1 && q_heads % kv_heads == 0 &&
+         kv8_padded_dim(head_dim) != 0 &&
+         (int64_t)min(max_q, tokens) * (q_heads / kv_heads) <= 0x7fffffff / 2;
+}
+
+extern "C" size_t paged_attn_kv8_workspace_bytes(int batch, int tokens, int max_q, int max_kv,
+                                                 int q_heads, int kv_heads, int head_dim) {
+  if (!attn_sizes_ok(batch, tokens, max_q, max_kv, q_heads, kv_heads, head_dim)) return 0;
+  if (batch == 0 || tokens == 0 || max_q == 0) return 0;
+  return attn_plan(batch, min(max_q, tokens), max_kv, q_heads / kv_heads, kv_heads,
+                   kv8_padded_dim(head_dim)).ws;
+}
+
+extern "C" int paged_attn_kv8(const uint16_t* q, int64_t q_stride, const void* k_codes,
+                              const void* v_codes, const float* k_scale, const float* v_scale,
+                              const int32_t* q_indptr, const int32_t* kv_len,
+                              const int32_t* page_table, int batch, int tokens, int max_q,
+                              int max_kv, int table_cols, int q_heads, int kv_heads, int head_dim,
+                              int page_size, int num_pages, int q_dtype, float sm_scale,
+                              uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+  if (q_dtype != W4_Q_I8 && q_dtype != W4_Q_F8) return W4_ERR_ARG;
+  if (!(sm_scale > -3.0e38f && sm_scale < 3.0e38f)) return W4_ERR_ARG;
+  if (!attn_sizes_ok(batch, tokens, max_q, max_kv, q_heads, kv_heads, head_dim) ||
+      table_cols < 1 || !kv8_page_ok(page_size) || num_pages < 1 ||
+      q_stride < (int64_t)q_heads * head_dim || q_stride % 4 || (!q_indptr && tokens != batch))
+    return W4_ERR_SHAPE;
+  if (batch == 0 || tokens == 0 || max_q == 0) return W4_OK;
+  if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !kv_len || !page_table || !out)
+    return W4_ERR_NULL;
+  if (!aligned(q, 8) || !aligned(out, 8) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(kv_len, 4) ||
+      !aligned(page_table, 4) || !aligned(q_indptr, 4) || !aligned(lse, 4) ||
+      !aligned(workspace, 256))
+    return W4_ERR_ALIGN;
+  AttnParams p{};
+  p.max_q = min(max_q, tokens);
+  const int dp = kv8_padded_dim(head_dim);
+  const AttnPlan a = attn_plan(batch, p.max_q, max_kv, q_heads / kv_heads, kv_heads, dp);
+  if (a.ws > 0 && (!workspace || workspace_bytes < a.ws)) return W4_ERR_WORKSPACE;
+  p.q = q, p.q_stride = q_stride;
+  p.kc = (const uint8_t*)k_codes, p.vc = (const uint8_t*)v_codes, p.ks = k_scale, p.vs = v_scale;
+  p.indptr = q_indptr, p.kv_len = kv_len, p.table = page_table;
+  p.out = out, p.lse = lse;
+  p.counters = (uint32_t*)workspace;
+  p.part = workspace ? (float*)((uint8_t*)workspace + WS_COUNTERS) : nullptr;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.batch = batch, p.tokens = tokens, p.max_kv = max_kv, p.cols = table_cols;
+  p.q_heads = q_heads, p.kv_heads = kv_heads, p.group = q_heads / kv_heads, p.dim = head_dim;
+  p.page_shift = __builtin_ctz(page_size), p.pages = num_pages;
+  p.tiles = a.tiles, p.chunk = a.chunk, p.splits = a.splits;
+#define W4_DP(D)                                                  \
+  case D:                                                         \
+    return q_dtype == W4_Q_I8 ? launch_attn<D, W4_Q_I8>(p, a, stream) \
+                              : launch_attn<D, W4_Q_F8>(p, a, stream)
+  switch (dp) {
+    W4_DP(64);
+    W4_DP(96);
+    W4_DP(128);
+    W4_DP(192);
+    default:
+      return q_dtype == W4_Q_I8 ? launch_attn<256, W4_Q_I8>(p, a, stream)
+                                : launch_attn<256, W4_Q_F8>(p, a, stream);
+  }
+#undef W4_DP
+}

@@ -1,0 +1,193 @@
+// Residual addition + root-mean-square norm + per-row 8-bit codes.
+//
+// One pass: with h = x + residual, g = h * weight, the row needs
+// S = sum h^2 and G = max |g|. The normalised row is y = g * r, r =
+// 1/sqrt(S/K + eps), its scale max|y|/L = G * r / L (L = 127 or 448), and the
+// codes y / scale = g * (L / G): the root cancels, so both reductions are
+// taken together and the row is coded from the registers it was loaded into.
+// Bound: bytes (fp16 with residual: 4 read, 3 written per element).
+
+#include "layer_common.hpp"
+
+namespace w4 {
+
+// One row per group of WAVES waves; CPT > 0: CPT chunks of 8 elements per lane
+// held in registers (K <= 512 * WAVES * CPT), loads of every chunk issued
+// before any is used. CPT == 0: rows too long for that are read three times
+// (the later reads come from L2), the residual sum being written by the last.
+// A block of 256 threads holds 4 / WAVES rows; longer rows take one block.
+template <typename T, int Q, int WAVES, int CPT>
+__global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void k_add_rmsnorm(
+    const T* X, const T* R, const T* __restrict__ Wt, int M, int K, float eps, T* H,
+    uint8_t* __restrict__ Yq, float* __restrict__ scale) {
+  constexpr int ROWS = WAVES < 4 ? 4 / WAVES : 1;
+  constexpr int LANES = 64 * WAVES;
+  __shared__ float shs[WAVES < 4 ? 4 : WAVES];
+  __shared__ uint32_t shm[WAVES < 4 ? 4 : WAVES];
+  const int tid = threadIdx.x % LANES;
+  const int sub = threadIdx.x / LANES;
+  // rows past the end repeat the last row up to its barriers and store nothing
+  const int mrow = blockIdx.x * ROWS + sub;
+  const bool live = mrow < M;
+  const int m = live ? mrow : M - 1;
+  const size_t base = (size_t)m * K;
+  const T* x = X + base;
+  const T* r = R ? R + base : nullptr;
+  const int nch = K / 8;
+
+  float ss = 0.f;
+  uint32_t mx = 0;
+  float h[CPT > 0 ? CPT : 1][8], g[CPT > 0 ? CPT : 1][8];
+  if constexpr (CPT > 0) {
+    // chunks past the row re-read its last chunk and count as zero, so that
+    // no load waits inside a branch
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) load8f(x + 8 * min(tid + i * LANES, nch - 1), h[i]);
+    float b[CPT][8];
+    if (R) {
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) load8f(r + 8 * min(tid + i * LANES, nch - 1), b[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) load8f(Wt + 8 * min(tid + i * LANES, nch - 1), g[i]);
+    if (R) {
+#pragma unroll
+      for (int i = 0; i < CPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] += b[i][e];
+    }
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const bool in = tid + i * LANES < nch;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        g[i][e] = in ? g[i][e] * h[i][e] : 0.f;
+        ss += in ? h[i][e] * h[i][e] : 0.f;
+        mx = max(mx, abs_bits(g[i][e]));
+      }
+    }
+  } else {
+    for (int c = tid; c < nch; c += LANES) {
+      float a[8], w[8];
+      load8f(x + 8 * c, a);
+      load8f(Wt + 8 * c, w);
+      if (R) {
+        float b[8];
+        load8f(r + 8 * c, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += b[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ss += a[e] * a[e];
+        mx = max(mx, abs_bits(a[e] * w[e]));
+      }
+    }
+  }
+  ss = wave_sum_f(ss);
+  mx = wave_max_u(mx);
+  if constexpr (WAVES > 1) {
+    const int wv = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      shs[wv] = ss;
+      shm[wv] = mx;
+    }
+    __syncthreads();
+    ss = 0.f;
+    mx = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+      ss += shs[sub * WAVES + i];
+      mx = max(mx, shm[sub * WAVES + i]);
+    }
+  }
+  constexpr float L = Q == W4_Q_I8 ? 127.f : 448.f;
+  const float gm = __uint_as_float(mx);
+  const float root = 1.0f / sqrtf(ss / (float)K + eps);
+  // a row whose largest product is below 2^-64 is coded after a multiplication
+  // by 2^64, so that L / G stays finite
+  const float up = gm < 0x1p-64f ? 0x1p64f : 1.0f;
+  const bool bad = mx >= F32_INF;
+  const float inv = bad || mx == 0 ? 0.f : L / (gm * up);
+  if (live && tid == 0)
+    scale[m] = bad ? __uint_as_float(0x7FC00000u) : gm * root / L;
+  uint8_t* out = Yq + base;
+  auto emit = [&](int c, const float (&v)[8]) {
+    u2 w = {0u, 0u};
+    if (!bad) {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = v[e] * up * inv;
+      w = u2{code4<Q>(y[0], y[1], y[2], y[3]), code4<Q>(y[4], y[5], y[6], y[7])};
+    }
+    *reinterpret_cast<u2*>(out + 8 * c) = w;
+  };
+  if constexpr (CPT > 0) {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int c = tid + i * LANES;
+      if (live && c < nch) {
+        if (H) store8f(H + base + 8 * c, h[i]);
+        emit(c, g[i]);
+      }
+    }
+  } else {
+    for (int c = tid; c < nch; c += LANES) {
+      float a[8], w[8];
+      load8f(x + 8 * c, a);
+      load8f(Wt + 8 * c, w);
+      if (R) {
+        float b[8];
+        load8f(r + 8 * c, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += b[e];
+      }
+      if (!live) continue;
+      if (H) store8f(H + base + 8 * c, a);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[e] *= w[e];
+      emit(c, a);
+    }
+  }
+}
+
+template <typename T, int Q>
+int launch_norm(const void* X, const void* R, const void* Wt, int M, int K, float eps, void* H,
+                void* Yq, float* scale, hipStream_t stream) {
+#define W4_NORM(WV, C)                                                                           \
+  hipLaunchKernelGGL((k_add_rmsnorm<T, Q, WV, C>), dim3(ceil_div(M, WV < 4 ? 4 / WV : 1)),       \
+                     dim3(WV < 4 ? 256 : 64 * WV), 0, stream, (const T*)X, (const T*)R,          \
+                     (const T*)Wt, M, K, eps, (T*)H, (uint8_t*)Yq, scale)
+  if (K <= 1024) W4_NORM(1, 2);
+  else if (K <= 4096) W4_NORM(4, 2);
+  else if (K <= 8192) W4_NORM(8, 2);
+  else if (K <= 16384) W4_NORM(16, 2);
+  else W4_NORM(16, 0);
+#undef W4_NORM
+  return launch_status();
+}
+
+}  // namespace w4
+
+using namespace w4;
+
+extern "C" int add_rmsnorm_q8(const void* X, const void* residual, const void* weight, int in_dtype,
+                              int M, int K, float eps, int q_dtype, void* residual_out, void* Yq,
+                              float* y_scale, hipStream_t stream) {
+  if (in_dtype != W4_IN_F16 && in_dtype != W4_IN_F32) return W4_ERR_ARG;
+  if (q_dtype != W4_Q_I8 && q_dtype != W4_Q_F8) return W4_ERR_ARG;
+  if (!(eps >= 0.f) || eps > 3.0e38f) return W4_ERR_ARG;
+  if (M < 0 || K < 8 || K % 8 || K > W4_MAX_K) return W4_ERR_SHAPE;
+  if (M == 0) return W4_OK;
+  if (!X || !weight || !Yq || !y_scale) return W4_ERR_NULL;
+  if (!aligned(X, 16) || !aligned(residual, 16) || !aligned(weight, 16) ||
+      !aligned(residual_out, 16) || !aligned(Yq, 16) || !aligned(y_scale, 4))
+    return W4_ERR_ALIGN;
+  auto go = [&](auto launch) {
+    return launch(X, residual, weight, M, K, eps, residual_out, Yq, y_scale, stream);
+  };
+  if (in_dtype == W4_IN_F16)
+    return q_dtype == W4_Q_I8 ? go(launch_norm<uint16_t, W4_Q_I8>)
+                              : go(launch_norm<uint16_t, W4_Q_F8>);
+  return q_dtype == W4_Q_I8 ? go(launch_norm<float, W4_Q_I8>) : go(launch_norm<float, W4_Q_F8>);
+}

@@ -13,3 +13,7 @@ one function whose parity is unpinned.
 """
 from .w4_oracle import *  # noqa: F401,F403
 from .w4_oracle import __all__  # noqa: F401
+from .layer_oracle import *  # noqa: F401,F403
+from .layer_oracle import __all__ as _layer_all
+
+__all__ = [*__all__, *_layer_all]
