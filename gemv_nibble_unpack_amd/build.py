@@ -4,10 +4,12 @@
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,10 @@ SOURCES = ["quant.hip", "prepack.hip", "matmul.hip", "gemm_launch.hip", "probe.h
 LAYER_CSRC = os.path.join(HERE, "csrc_layer")
 LAYER_SOURCES = ["norm.hip", "append.hip", "attn.hip"]
 OUT = os.path.join(HERE, "libgemv_nibble_unpack.so")
+# the Python marshalling of the decoder-layer operators: host code, built
+# against torch's headers, linked to OUT beside it
+BIND_SOURCE = os.path.join(LAYER_CSRC, "bind.cpp")
+BIND_OUT = os.path.join(HERE, "_layer_bind.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 ARCH = os.environ.get("W4_OFFLOAD_ARCH", "gfx950")
 
@@ -66,6 +72,8 @@ def build(verbose=True, jobs=None):
     objs = [os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(s))[0] + ".o") for s in srcs]
     cflags = [f for f in FLAGS if f != "-shared"]
     cmds = [[hipcc(), *cflags, *inc, "-c", s, "-o", o] for s, o in zip(srcs, objs)]
+    bind_obj = os.path.join(OBJ_DIR, "bind.o")
+    cmds.append(bind_compile(bind_obj))
     jobs = jobs or min(len(cmds), max(1, (os.cpu_count() or 1)))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         for f in [ex.submit(_run, c, verbose) for c in cmds]:
@@ -74,7 +82,37 @@ def build(verbose=True, jobs=None):
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
     undefined_kernels(tmp)
     os.replace(tmp, OUT)
+    _run(bind_link(bind_obj, BIND_OUT + ".tmp"), verbose)
+    os.replace(BIND_OUT + ".tmp", BIND_OUT)
     return OUT
+
+
+def _cxx():
+    for c in (os.environ.get("CXX"), shutil.which("g++"), shutil.which("c++")):
+        if c and shutil.which(c):
+            return c
+    raise RuntimeError("no host C++ compiler found")
+
+
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")          # its place, without importing it
+    return os.path.dirname(spec.origin)
+
+
+def bind_compile(obj):
+    """The command that compiles the marshalling module (host code only)."""
+    inc = os.path.join(_torch_dir(), "include")
+    return [_cxx(), "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+            "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", os.path.join(ROOT, "include"), "-isystem", inc,
+            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
+            os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"), "-I",
+            sysconfig.get_paths()["include"], "-c", BIND_SOURCE, "-o", obj]
+
+
+def bind_link(obj, out):
+    return [_cxx(), "-shared", "-fPIC", obj, "-o", out, f"-L{HERE}", f"-l:{os.path.basename(OUT)}",
+            "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(_torch_dir(), 'lib')}", "-ltorch_python",
+            "-ltorch_hip", "-ltorch_cpu", "-lc10_hip", "-lc10"]
 
 
 def undefined_kernels(path):
