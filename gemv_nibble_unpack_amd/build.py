@@ -20,7 +20,7 @@ SOURCES = ["quant.hip", "prepack.hip", "matmul.hip", "gemm_launch.hip", "probe.h
 # the decoder-layer operators, beside csrc: the traffic records of the matmul
 # kernels carry a hash over csrc, which these sources do not change
 LAYER_CSRC = os.path.join(HERE, "csrc_layer")
-LAYER_SOURCES = ["norm.hip", "append.hip", "attn.hip"]
+LAYER_SOURCES = ["norm.hip", "append.hip", "attn.hip", "attn_many.hip"]
 OUT = os.path.join(HERE, "libgemv_nibble_unpack.so")
 # the Python marshalling of the decoder-layer operators: host code, built
 # against torch's headers, linked to OUT beside it

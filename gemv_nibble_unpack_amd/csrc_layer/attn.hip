@@ -381,7 +381,8 @@ __global__ __launch_bounds__(256) void k_attn_few(const AttnParams p) {
 // The launch for these sizes: rows per tile, tiles, chunk and splits, and the
 // workspace they need.
 struct AttnPlan {
-  int qt, tiles, chunk, splits;
+  bool many;                       // k_attn_many
+  int qt, tiles, chunk, splits, fold;
   int64_t units;
   size_t ws;
 };
@@ -389,16 +390,22 @@ struct AttnPlan {
 inline AttnPlan attn_plan(int batch, int max_q, int max_kv, int group, int kv_heads, int dp) {
   AttnPlan a{};
   const int64_t rows = (int64_t)max_q * group;
+  a.many = rows > 32;
   a.qt = rows > 16 ? 2 : 1;
-  a.tiles = (int)((rows + 16 * a.qt - 1) / (16 * a.qt));
+  const int tile = a.many ? MANY_ROWS : 16 * a.qt;
+  a.tiles = (int)((rows + tile - 1) / tile);
   a.units = (int64_t)batch * kv_heads * a.tiles;
+  const int64_t least = a.many ? 512 : 256, blocks = a.many ? 448 : 1024;
   int64_t splits = 1;
   if (a.units <= WS_COUNTER_SLOTS)
-    splits = max((int64_t)1, min((int64_t)(max_kv + 255) / 256, 1024 / a.units));
+    splits = max((int64_t)1, min((max_kv + least - 1) / least, blocks / a.units));
   a.chunk = (int)(((max_kv + splits - 1) / splits + 255) / 256 * 256);
   a.splits = max(1, (max_kv + a.chunk - 1) / a.chunk);
+  // few enough blocks that all run at once (two a CU): the second half of the
+  // tiles in rising order, so that a CU's two blocks add up to the same work
+  a.fold = a.many && a.units * a.splits <= 512;
   a.ws = a.splits == 1 ? 0
-                       : WS_COUNTERS + (size_t)a.units * a.splits * 16 * a.qt * (dp + 2) * 4;
+                       : WS_COUNTERS + (size_t)a.units * a.splits * tile * (dp + (a.many ? 4 : 2)) * 4;
   return a;
 }
 
@@ -476,7 +483,11 @@ extern "C" int paged_attn_kv8(const uint16_t* q, int64_t q_stride, const void* k
   p.batch = batch, p.tokens = tokens, p.max_kv = max_kv, p.cols = table_cols;
   p.q_heads = q_heads, p.kv_heads = kv_heads, p.group = q_heads / kv_heads, p.dim = head_dim;
   p.page_shift = __builtin_ctz(page_size), p.pages = num_pages;
-  p.tiles = a.tiles, p.chunk = a.chunk, p.splits = a.splits;
+  p.tiles = a.tiles, p.chunk = a.chunk, p.splits = a.splits, p.fold = a.fold;
+  if (a.many) {
+    if (a.units * a.splits > 0x7fffff) return W4_ERR_SHAPE;
+    return launch_attn_many(p, dp, q_dtype, a.units * a.splits, stream);
+  }
 #define W4_DP(D)                                                  \
   case D:                                                         \
     return q_dtype == W4_Q_I8 ? launch_attn<D, W4_Q_I8>(p, a, stream) \

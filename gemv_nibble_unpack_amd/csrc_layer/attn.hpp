@@ -22,7 +22,11 @@ struct AttnParams {
   int page_shift, pages;
   int tiles;                // row tiles of max_q * group rows
   int chunk, splits;        // cached tokens per block (a multiple of 64), blocks along them
+  int fold;                 // many rows: order of the row tiles (see k_attn_many)
 };
+
+constexpr int MANY_ROWS = 128;    // query rows of a block of k_attn_many
+int launch_attn_many(const AttnParams& p, int dp, int kind, int64_t blocks, hipStream_t stream);
 
 // Sequence b's query rows and cached length. False: no new tokens, or ones
 // outside the inputs. `fits` false: the lengths contradict each other or the

@@ -1,0 +1,383 @@
+// Attention of many new tokens (prompts, chunks of prompts) over the paged
+// 8-bit cache.
+//
+// A block takes 128 query rows of a (sequence, kv head), 32 for each of its
+// four waves, and walks the cached tokens that its last row sees in steps of
+// 64. The step's codes are read once per block, widened to fp16 (exact) and
+// laid in LDS in the order in which the matrix instructions read them; the
+// next step's codes are in flight meanwhile (registers, then the other of two
+// LDS stages). Per wave and step, with v_mfma_f32_32x32x16_f16:
+//
+//   S^T = K q^T    64 tokens x 32 rows
+//   w   = 2^(S a - m) * v_scale / r    one fma and one exponential an element
+//   O^T += V^T w^T
+//
+// Token order: row i = 8 x + 4 g + y of a K operand is token 16 g + 4 x + y of its
+// 32, so that lane (column c, half g) of the product holds the 16 consecutive
+// tokens 16 g .. 16 g + 15 of one page (one key and one value scale a lane), which
+// are, 8 at a time, the k slots that the same lane feeds to the second product:
+// the weights never leave their registers.
+//
+// The running maximum is raised (and O, the sum rescaled) only when a row's
+// new maximum exceeds it by more than 8 in log2 units, or a larger value
+// scale arrives; until then weights stay below 2^8, which P_UP_MANY = 2^7
+// keeps inside fp16 with room to spare. r is the largest value scale met.
+
+#include "attn.hpp"
+
+namespace w4 {
+
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+constexpr float P_UP_MANY = 128.0f, LOG2_P_UP_MANY = 7.0f;
+constexpr float M_SLACK = 8.0f;
+constexpr float REF_MIN_MANY = 0x1p-100f;
+constexpr float RATIO_MIN = 0x1p-40f;     // smaller value scales count as this times r
+
+template <int DP>
+struct AttnMany {
+  static constexpr int STEP = 64, ROWS = MANY_ROWS;
+  static constexpr int KS = DP / 16;                 // k steps of the first product
+  static constexpr int DT = DP / 32;                 // dim tiles of the second
+  static constexpr int CH = 4 * DP;                  // 16-code chunks of K (and of V) a step
+  static constexpr int PER = (CH + 255) / 256;       // chunks per thread
+  // a fragment: 64 lanes x 16 bytes as [row][half]; 32 bytes apart, so that
+  // both the stores of a wave and its reads touch every bank once
+  static constexpr int FRAG = 1024 + 32;
+  static constexpr int K_FRAGS = 2 * KS, V_FRAGS = 4 * DT;
+  static constexpr int STAGE = (K_FRAGS + V_FRAGS) * FRAG;
+  static constexpr int LDS = 2 * STAGE + 16;
+};
+
+template <int DP, int Q>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_attn_many(const AttnParams p) {
+  using C = AttnMany<DP>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  unsigned* slast = reinterpret_cast<unsigned*>(smem + 2 * C::STAGE);
+
+  // heads fastest (a head's blocks share an XCD's L2 when kv_heads is a
+  // multiple of 8), then splits and sequences, row tiles slowest: the longest
+  // first, or folded (see attn_many_plan)
+  int t = blockIdx.x;
+  const int h = t % p.kv_heads;
+  t /= p.kv_heads;
+  const int split = t % p.splits;
+  t /= p.splits;
+  const int b = t % p.batch;
+  const int k = t / p.batch;
+  const int half = (p.tiles + 1) / 2;
+  const int tile = !p.fold || k < half ? p.tiles - 1 - k : k - half;
+
+  int row0, n, len;
+  bool fits;
+  if (!attn_span(p, b, row0, n, len, fits)) return;
+  const int rows = min(n, p.max_q) * p.group;
+  const int r0 = tile * C::ROWS;
+  if (r0 >= rows) return;
+  const int nr = min(rows - r0, C::ROWS);
+  const int first = len - n;
+  const int seen = fits ? max(0, first + (r0 + nr - 1) / p.group + 1) : 0;
+  const int parts = max(1, (seen + p.chunk - 1) / p.chunk);
+  if (split >= parts) return;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 31, g = lane >> 5;
+  const int P = 1 << p.page_shift;
+  const int32_t* tab = p.table + (size_t)b * p.cols;
+  const int c0 = split * p.chunk, c1 = min(seen, c0 + p.chunk);
+  const int last16 = (max(seen, 1) - 1) & ~15;
+
+  // ---- this lane's query row ---------------------------------------------
+  const int wr = r0 + 32 * wave;                     // the wave's first row
+  const int r = wr + c;
+  const int rc = r < rows ? r : rows - 1;
+  const int tok = rc / p.group, hh = h * p.group + (rc - tok * p.group);
+  const int lim = r < rows && fits ? first + tok + 1 : 0;
+  // tokens that every / some row of the wave sees
+  const int lim_all = wr + 31 < rows && fits ? first + wr / p.group + 1 : 0;
+  const int lim_any = wr < rows && fits ? first + (min(wr + 31, rows - 1)) / p.group + 1 : 0;
+  h8 qf[C::KS];
+  {
+    const uint16_t* q = p.q + (int64_t)(row0 + tok) * p.q_stride + (int64_t)hh * p.dim;
+    auto quad = [&](int d) {
+      return d < p.dim ? *reinterpret_cast<const u2*>(q + d) : u2{0u, 0u};
+    };
+#pragma unroll
+    for (int s = 0; s < C::KS; ++s) {
+      const u2 x = quad(16 * s + 8 * g), y = quad(16 * s + 8 * g + 4);
+      qf[s] = __builtin_bit_cast(h8, u4{x[0], x[1], y[0], y[1]});
+    }
+  }
+
+  // ---- one step's codes: registers, then LDS ------------------------------
+  u4 kraw[C::PER], vraw[C::PER];
+  float ksc[2], vsc[2];                              // scales of the lane's token groups
+  // group `gi` of the step at t0 (16 tokens): its page and first slot; groups
+  // past the last visible token repeat the last one
+  auto page_of = [&](int t0, int gi, int& slot, bool& ok) {
+    const int tk = min(t0 + 16 * gi, last16);
+    const int id = tab[tk >> p.page_shift];
+    slot = tk & (P - 1);
+    ok = id >= 0 && id < p.pages;
+    return ok ? id : 0;
+  };
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < C::PER; ++i) {
+      const int idx = tid + 256 * i;
+      if (C::CH % 256 == 0 || idx < C::CH) {
+        const int tk = idx / (DP / 16), j = idx % (DP / 16);
+        int slot;
+        bool ok;
+        const int id = page_of(t0, tk >> 4, slot, ok);
+        kraw[i] = *reinterpret_cast<const u4*>(
+            p.kc + ((((size_t)id * p.kv_heads + h) << p.page_shift) + slot + (tk & 15)) * DP + 16 * j);
+        const int vg = idx & 3, d = idx >> 2;
+        const int iv = page_of(t0, vg, slot, ok);
+        vraw[i] = *reinterpret_cast<const u4*>(
+            p.vc + ((((size_t)iv * p.kv_heads + h) * DP + d) << p.page_shift) + slot);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      int slot;
+      bool ok;
+      const int id = page_of(t0, 2 * x + g, slot, ok);
+      const size_t at = (size_t)id * p.kv_heads + h;
+      ksc[x] = ok ? p.ks[at] : __uint_as_float(0x7FC00000u);
+      vsc[x] = p.vs[at];
+    }
+  };
+  auto stage = [&](int t0, uint8_t* s) {
+#pragma unroll
+    for (int i = 0; i < C::PER; ++i) {
+      const int idx = tid + 256 * i;
+      if (C::CH % 256 == 0 || idx < C::CH) {
+        {
+          const int tk = idx / (DP / 16), j = idx % (DP / 16);
+          const int y = tk & 15;
+          const int row = 8 * (y >> 2) + 4 * ((tk >> 4) & 1) + (y & 3);
+          h8* o = reinterpret_cast<h8*>(s + ((tk >> 5) * C::KS + j) * C::FRAG + row * 32);
+          o[0] = widen8<Q>(kraw[i][0], kraw[i][1]);
+          o[1] = widen8<Q>(kraw[i][2], kraw[i][3]);
+        }
+        const int vg = idx & 3, d = idx >> 2;
+        u4 v = vraw[i];
+        // codes past the length may be E4M3 NaNs: 0 * NaN would reach the sums
+        if (Q == W4_Q_F8 && t0 + C::STEP > seen) {
+          const int left = min(max(seen - t0 - 16 * vg, 0), 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = min(max(left - 4 * e, 0), 4);
+            v[e] &= x == 4 ? 0xFFFFFFFFu : (1u << (8 * x)) - 1u;
+          }
+        }
+        uint8_t* o = s + (C::K_FRAGS + (d >> 5) * 4 + (vg >> 1) * 2) * C::FRAG + (d & 31) * 32 +
+                     (vg & 1) * 16;
+        *reinterpret_cast<h8*>(o) = widen8<Q>(v[0], v[1]);
+        *reinterpret_cast<h8*>(o + C::FRAG) = widen8<Q>(v[2], v[3]);
+      }
+    }
+  };
+
+  f16v o[C::DT];
+  float m = -__builtin_inff(), l = 0.f, ref = REF_MIN_MANY;
+#pragma unroll
+  for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+
+  auto step = [&](int t0, const uint8_t* s, const float (&sk)[2], const float (&sv)[2]) {
+    const uint8_t* fr = s + c * 32 + g * 16;
+    f16v x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[i][e] = 0.f;
+#pragma unroll
+      for (int q = 0; q < C::KS; ++q)
+        x[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            *reinterpret_cast<const h8*>(fr + (i * C::KS + q) * C::FRAG), qf[q], x[i], 0, 0, 0);
+    }
+    const int left0 = lim - t0 - 16 * g;             // of tile 0's 16 tokens, and 32 less of tile 1's
+    float a[2], mx = -__builtin_inff(), rmax = ref;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i] = sk[i] * p.scale_log2;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[i][e] *= a[i];
+      if (t0 + C::STEP > lim_all) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[i][e] = e < left0 - 32 * i ? x[i][e] : -__builtin_inff();
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[i][e]);
+      rmax = fmaxf(rmax, left0 - 32 * i > 0 ? sv[i] : 0.f);
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    if (__any(mx > m + M_SLACK || rmax > ref)) {
+      const float nm = fmaxf(m, mx);
+      const float base = nm == -__builtin_inff() ? 0.f : nm;
+      const float alpha = __builtin_amdgcn_exp2f(m - base);
+      // r is one value for the wave
+      float nr2 = rmax;
+#pragma unroll
+      for (int w = 32; w; w >>= 1) nr2 = fmaxf(nr2, __shfl_xor(nr2, w, 64));
+      const float f = alpha * (ref / nr2);
+      m = nm;
+      ref = nr2;
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] *= f;
+    }
+    const float base = m == -__builtin_inff() ? 0.f : m;
+    h8 w[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // weight in units of r; a page that the row does not see may have any scale
+      float ratio = sv[i] / ref;
+      ratio = ratio < RATIO_MIN ? RATIO_MIN : ratio;
+      ratio = left0 - 32 * i > 0 ? ratio : 1.f;
+      const float shift = __builtin_amdgcn_logf(ratio) + LOG2_P_UP_MANY - base;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float y = __builtin_amdgcn_exp2f(x[i][e] + shift);
+        sum += y;
+        w[i][e >> 3][e & 7] = (_Float16)y;
+      }
+      l += sum / ratio;
+    }
+#pragma unroll
+    for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              *reinterpret_cast<const h8*>(fr + (C::K_FRAGS + 4 * d + 2 * i + u) * C::FRAG),
+              w[i][u], o[d], 0, 0, 0);
+  };
+
+  if (c0 < c1) {
+    load(c0);
+    stage(c0, smem);
+    float sk[2] = {ksc[0], ksc[1]}, sv[2] = {vsc[0], vsc[1]};
+    __syncthreads();
+    int buf = 0;
+    for (int t0 = c0; t0 < c1; t0 += C::STEP) {
+      const bool more = t0 + C::STEP < c1;
+      if (more) load(t0 + C::STEP);
+      if (t0 < lim_any) step(t0, smem + buf * C::STAGE, sk, sv);
+      if (more) {
+        stage(t0 + C::STEP, smem + (buf ^ 1) * C::STAGE);
+        sk[0] = ksc[0], sk[1] = ksc[1], sv[0] = vsc[0], sv[1] = vsc[1];
+      }
+      __syncthreads();
+      buf ^= 1;
+    }
+  }
+  l = (l + __shfl_xor(l, 32, 64)) * (1.0f / P_UP_MANY);
+
+  // ---- results: lane (c, g) holds dims 32 d + 8 x + 4 g + y of row r ---------
+  auto put = [&](float M, float L, float up) {       // up: o's units over L's
+    if (r >= rows) return;
+    const size_t at = (size_t)(row0 + tok) * p.q_heads + hh;
+    const float nan = __uint_as_float(0x7FC00000u);
+    const float inv = !fits ? nan : L == 0.f ? 0.f : up / L;
+#pragma unroll
+    for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int dim = 32 * d + 8 * q + 4 * g;
+        const h4 y = {(_Float16)(o[d][4 * q] * inv), (_Float16)(o[d][4 * q + 1] * inv),
+                      (_Float16)(o[d][4 * q + 2] * inv), (_Float16)(o[d][4 * q + 3] * inv)};
+        if (dim < p.dim)
+          *reinterpret_cast<u2*>(p.out + at * p.dim + dim) = __builtin_bit_cast(u2, y);
+      }
+    if (p.lse && g == 0)
+      p.lse[at] = !fits ? nan : L == 0.f ? -__builtin_inff()
+                                         : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+  };
+  if (parts == 1) {
+    put(m, l, ref * (1.0f / P_UP_MANY));
+    return;
+  }
+
+  // ---- chunks joined by the block that arrives last (as in attn.hip); a part
+  // is the block's registers in lane order, O in absolute units, then (M, L)
+  const size_t unit = ((size_t)b * p.kv_heads + h) * p.tiles + tile;
+  constexpr size_t PART = (size_t)256 * (C::DT * 16 + 2);
+  uint32_t* po = reinterpret_cast<uint32_t*>(p.part) + unit * p.splits * PART + 2 * tid;
+  {
+    uint32_t* q = po + split * PART;
+    const float up = ref * (1.0f / P_UP_MANY);
+#pragma unroll
+    for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; e += 2)
+        dev_store2(q + (d * 8 + e / 2) * 512, __float_as_uint(o[d][e] * up),
+                   __float_as_uint(o[d][e + 1] * up));
+    dev_store2(q + C::DT * 8 * 512, __float_as_uint(m), __float_as_uint(l));
+  }
+  stores_done();
+  __syncthreads();
+  if (tid == 0) *slast = dev_arrive(p.counters + unit) == (unsigned)(parts - 1);
+  __syncthreads();
+  if (!*slast) return;
+  if (tid == 0) dev_store(p.counters + unit, 0u);
+  float M = -__builtin_inff(), L = 0.f;
+  for (int z = 0; z < parts; ++z) {
+    const uint64_t ml = dev_load2(po + z * PART + C::DT * 8 * 512);
+    const float Mz = __uint_as_float((uint32_t)ml), Lz = __uint_as_float((uint32_t)(ml >> 32));
+    const float nm = fmaxf(M, Mz);
+    const float base = nm == -__builtin_inff() ? 0.f : nm;
+    const float fo = z ? __builtin_amdgcn_exp2f(M - base) : 0.f;
+    const float fn = __builtin_amdgcn_exp2f(Mz - base);
+    M = nm;
+    L = L * fo + Lz * fn;
+#pragma unroll
+    for (int d = 0; d < C::DT; ++d) {
+      uint64_t v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = dev_load2(po + z * PART + (d * 8 + e) * 512);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = __uint_as_float((uint32_t)v[e]), y = __uint_as_float((uint32_t)(v[e] >> 32));
+        o[d][2 * e] = z ? o[d][2 * e] * fo + x * fn : x * fn;
+        o[d][2 * e + 1] = z ? o[d][2 * e + 1] * fo + y * fn : y * fn;
+      }
+    }
+  }
+  put(M, L, 1.0f);
+}
+
+template <int DP, int Q>
+static int launch(const AttnParams& p, int64_t blocks, hipStream_t stream) {
+  constexpr int lds = AttnMany<DP>::LDS;
+  allow_smem((const void*)k_attn_many<DP, Q>, lds);
+  hipLaunchKernelGGL((k_attn_many<DP, Q>), dim3((unsigned)blocks), dim3(256), lds, stream, p);
+  return launch_status();
+}
+
+int launch_attn_many(const AttnParams& p, int dp, int kind, int64_t blocks, hipStream_t stream) {
+#define W4_DP(D)                                                       \
+  case D:                                                              \
+    return kind == W4_Q_I8 ? launch<D, W4_Q_I8>(p, blocks, stream)     \
+                           : launch<D, W4_Q_F8>(p, blocks, stream)
+  switch (dp) {
+    W4_DP(64);
+    W4_DP(96);
+    W4_DP(128);
+    W4_DP(192);
+    default:
+      return kind == W4_Q_I8 ? launch<256, W4_Q_I8>(p, blocks, stream)
+                             : launch<256, W4_Q_F8>(p, blocks, stream);
+  }
+#undef W4_DP
+}
+
+}  // namespace w4
