@@ -100,7 +100,8 @@ __global__ __launch_bounds__(256) void k_attn_few(const AttnParams p) {
     lim[u] = in && fits ? first + tok + 1 : 0;
     const uint16_t* q = p.q + (int64_t)(row0 + tok) * p.q_stride + (int64_t)hh * p.dim;
     auto quad = [&](int d) {                         // dims past the head are zero
-      return d < p.dim ? *reinterpret_cast<const u2*>(q + d) : u2{0u, 0u};
+      const u2 x = d < p.dim ? *reinterpret_cast<const u2*>(q + d) : u2{0u, 0u};
+      return u2{x[0] ^ p.q_sign, x[1] ^ p.q_sign};
     };
     auto oct = [&](int d) {
       const u2 a = quad(d), b2 = quad(d + 4);
@@ -479,7 +480,8 @@ extern "C" int paged_attn_kv8(const uint16_t* q, int64_t q_stride, const void* k
   p.out = out, p.lse = lse;
   p.counters = (uint32_t*)workspace;
   p.part = workspace ? (float*)((uint8_t*)workspace + WS_COUNTERS) : nullptr;
-  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.scale_log2 = fabsf(sm_scale) * 1.4426950408889634f;
+  p.q_sign = sm_scale < 0.f ? 0x80008000u : 0u;
   p.batch = batch, p.tokens = tokens, p.max_kv = max_kv, p.cols = table_cols;
   p.q_heads = q_heads, p.kv_heads = kv_heads, p.group = q_heads / kv_heads, p.dim = head_dim;
   p.page_shift = __builtin_ctz(page_size), p.pages = num_pages;

@@ -16,7 +16,8 @@ struct AttnParams {
   float* lse;
   uint32_t* counters;       // split launches: arrivals per (sequence, head, row tile)
   float* part;              // split launches: partial results
-  float scale_log2;         // softmax scale * log2(e)
+  float scale_log2;         // |softmax scale| * log2(e)
+  uint32_t q_sign;          // 0x80008000 if the softmax scale is negative: flips a pair of q's
   int batch, tokens, max_q, max_kv, cols;
   int q_heads, kv_heads, group, dim;
   int page_shift, pages;

@@ -106,47 +106,51 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_attn_many(const Attn
 #pragma unroll
     for (int s = 0; s < C::KS; ++s) {
       const u2 x = quad(16 * s + 8 * g), y = quad(16 * s + 8 * g + 4);
-      qf[s] = __builtin_bit_cast(h8, u4{x[0], x[1], y[0], y[1]});
+      qf[s] = __builtin_bit_cast(h8, u4{x[0] ^ p.q_sign, x[1] ^ p.q_sign, y[0] ^ p.q_sign,
+                                        y[1] ^ p.q_sign});
     }
   }
 
   // ---- one step's codes: registers, then LDS ------------------------------
+  // Lane i of a wave holds group i & 3 (16 tokens) of a step: its page number,
+  // fetched two steps ahead, and its scales, fetched one step ahead. Groups past
+  // the last visible token repeat the last one.
   u4 kraw[C::PER], vraw[C::PER];
-  float ksc[2], vsc[2];                              // scales of the lane's token groups
-  // group `gi` of the step at t0 (16 tokens): its page and first slot; groups
-  // past the last visible token repeat the last one
-  auto page_of = [&](int t0, int gi, int& slot, bool& ok) {
-    const int tk = min(t0 + 16 * gi, last16);
-    const int id = tab[tk >> p.page_shift];
-    slot = tk & (P - 1);
-    ok = id >= 0 && id < p.pages;
-    return ok ? id : 0;
-  };
+  float ksl, vsl;
+  int idl;
+  auto slot_of = [&](int t0, int gi) { return min(t0 + 16 * gi, last16); };
+  auto load_ids = [&](int t0) { idl = tab[slot_of(t0, lane & 3) >> p.page_shift]; };
   auto load = [&](int t0) {
+    const bool ok = idl >= 0 && idl < p.pages;
+    const int id = ok ? idl : 0;
+    const size_t at = (size_t)id * p.kv_heads + h;
+    ksl = ok ? p.ks[at] : __uint_as_float(0x7FC00000u);
+    vsl = p.vs[at];
+    // byte offsets of the four groups' first slots (uniform), one picked per chunk
+    auto koff = [&](int gi) {
+      const size_t ph = (size_t)__builtin_amdgcn_readlane(id, gi) * p.kv_heads + h;
+      return ((ph << p.page_shift) + (slot_of(t0, gi) & (P - 1))) * DP;
+    };
+    auto voff = [&](int gi) {
+      const size_t ph = (size_t)__builtin_amdgcn_readlane(id, gi) * p.kv_heads + h;
+      return ((ph * DP) << p.page_shift) + (slot_of(t0, gi) & (P - 1));
+    };
+    const size_t k0 = koff(0), k1 = koff(1), k2 = koff(2), k3 = koff(3);
+    const size_t v0 = voff(0), v1 = voff(1), v2 = voff(2), v3 = voff(3);
+    auto pick = [](size_t x0, size_t x1, size_t x2, size_t x3, int gi) {
+      const size_t lo = gi & 1 ? x1 : x0, hi = gi & 1 ? x3 : x2;
+      return gi & 2 ? hi : lo;
+    };
+    const uint8_t* vp = p.vc + pick(v0, v1, v2, v3, tid & 3);
 #pragma unroll
     for (int i = 0; i < C::PER; ++i) {
       const int idx = tid + 256 * i;
       if (C::CH % 256 == 0 || idx < C::CH) {
         const int tk = idx / (DP / 16), j = idx % (DP / 16);
-        int slot;
-        bool ok;
-        const int id = page_of(t0, tk >> 4, slot, ok);
         kraw[i] = *reinterpret_cast<const u4*>(
-            p.kc + ((((size_t)id * p.kv_heads + h) << p.page_shift) + slot + (tk & 15)) * DP + 16 * j);
-        const int vg = idx & 3, d = idx >> 2;
-        const int iv = page_of(t0, vg, slot, ok);
-        vraw[i] = *reinterpret_cast<const u4*>(
-            p.vc + ((((size_t)iv * p.kv_heads + h) * DP + d) << p.page_shift) + slot);
+            p.kc + pick(k0, k1, k2, k3, tk >> 4) + (tk & 15) * DP + 16 * j);
+        vraw[i] = *reinterpret_cast<const u4*>(vp + ((size_t)(idx >> 2) << p.page_shift));
       }
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      int slot;
-      bool ok;
-      const int id = page_of(t0, 2 * x + g, slot, ok);
-      const size_t at = (size_t)id * p.kv_heads + h;
-      ksc[x] = ok ? p.ks[at] : __uint_as_float(0x7FC00000u);
-      vsc[x] = p.vs[at];
     }
   };
   auto stage = [&](int t0, uint8_t* s) {
@@ -182,7 +186,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_attn_many(const Attn
   };
 
   f16v o[C::DT];
-  float m = -__builtin_inff(), l = 0.f, ref = REF_MIN_MANY;
+  float m = -__builtin_inff(), l = 0.f, ref = REF_MIN_MANY, inv_ref = 1.0f / REF_MIN_MANY;
 #pragma unroll
   for (int d = 0; d < C::DT; ++d)
 #pragma unroll
@@ -190,29 +194,61 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_attn_many(const Attn
 
   auto step = [&](int t0, const uint8_t* s, const float (&sk)[2], const float (&sv)[2]) {
     const uint8_t* fr = s + c * 32 + g * 16;
+    auto frag = [&](int i) { return *reinterpret_cast<const h8*>(fr + i * C::FRAG); };
+    // Operand fragments come from LDS one group ahead of the products that
+    // take them; the scheduling barriers keep the compiler from sinking a
+    // group's reads down to their use, where each would be waited for alone.
     f16v x[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[i][e] = 0.f;
+    {
+      h8 f[2][4];
+      auto read = [&](int gq) {
 #pragma unroll
-      for (int q = 0; q < C::KS; ++q)
-        x[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            *reinterpret_cast<const h8*>(fr + (i * C::KS + q) * C::FRAG), qf[q], x[i], 0, 0, 0);
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) f[gq & 1][2 * q + i] = frag(i * C::KS + 2 * gq + q);
+      };
+      read(0);
+#pragma unroll
+      for (int gq = 0; gq < C::KS / 2; ++gq) {
+        if (gq + 1 < C::KS / 2) read(gq + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            x[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[gq & 1][2 * q + i], qf[2 * gq + q], x[i],
+                                                          0, 0, 0);
+      }
     }
+    h8 vf[2][C::DT];
+    auto readv = [&](int iu) {
+#pragma unroll
+      for (int d = 0; d < C::DT; ++d) vf[iu & 1][d] = frag(C::K_FRAGS + 4 * d + iu);
+    };
+    readv(0);
     const int left0 = lim - t0 - 16 * g;             // of tile 0's 16 tokens, and 32 less of tile 1's
+    if (t0 + C::STEP > lim_all) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[i][e] = e < left0 - 32 * i ? x[i][e] : -__builtin_inff();
+    }
+    // The factors a are not negative (a negative softmax scale has gone into
+    // q's sign), so a tile's largest product gives its largest score. A zero
+    // factor becomes 2^-126, which keeps a masked -inf what it is; a NaN scale
+    // stays NaN through the difference.
     float a[2], mx = -__builtin_inff(), rmax = ref;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      a[i] = sk[i] * p.scale_log2;
+      a[i] = fmaxf(sk[i] * p.scale_log2, 0x1p-126f) + (sk[i] - sk[i]);
+      float tm = x[i][0];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[i][e] *= a[i];
-      if (t0 + C::STEP > lim_all) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[i][e] = e < left0 - 32 * i ? x[i][e] : -__builtin_inff();
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[i][e]);
+      for (int e = 1; e < 16; ++e) tm = fmaxf(tm, x[i][e]);
+      mx = fmaxf(mx, tm * a[i]);
       rmax = fmaxf(rmax, left0 - 32 * i > 0 ? sv[i] : 0.f);
     }
     mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
@@ -227,6 +263,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_attn_many(const Attn
       const float f = alpha * (ref / nr2);
       m = nm;
       ref = nr2;
+      inv_ref = 1.0f / nr2;
       l *= alpha;
 #pragma unroll
       for (int d = 0; d < C::DT; ++d)
@@ -238,43 +275,57 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_attn_many(const Attn
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // weight in units of r; a page that the row does not see may have any scale
-      float ratio = sv[i] / ref;
+      float ratio = sv[i] * inv_ref;
       ratio = ratio < RATIO_MIN ? RATIO_MIN : ratio;
       ratio = left0 - 32 * i > 0 ? ratio : 1.f;
+      const float ai = left0 - 32 * i > 0 ? a[i] : 1.f;
       const float shift = __builtin_amdgcn_logf(ratio) + LOG2_P_UP_MANY - base;
       float sum = 0.f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float y = __builtin_amdgcn_exp2f(x[i][e] + shift);
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][e], ai, shift));
         sum += y;
         w[i][e >> 3][e & 7] = (_Float16)y;
       }
-      l += sum / ratio;
+      l += sum * __builtin_amdgcn_rcpf(ratio);
     }
 #pragma unroll
-    for (int d = 0; d < C::DT; ++d)
+    for (int iu = 0; iu < 4; ++iu) {
+      if (iu < 3) readv(iu + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-              *reinterpret_cast<const h8*>(fr + (C::K_FRAGS + 4 * d + 2 * i + u) * C::FRAG),
-              w[i][u], o[d], 0, 0, 0);
+      for (int d = 0; d < C::DT; ++d)
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[iu & 1][d], w[iu >> 1][iu & 1], o[d], 0, 0,
+                                                      0);
+    }
   };
 
   if (c0 < c1) {
+    float sk[2], sv[2];
+    auto scales = [&] {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        sk[x] = g ? lane_f(ksl, 2 * x + 1) : lane_f(ksl, 2 * x);
+        sv[x] = g ? lane_f(vsl, 2 * x + 1) : lane_f(vsl, 2 * x);
+      }
+    };
+    load_ids(c0);
     load(c0);
+    load_ids(c0 + C::STEP);
     stage(c0, smem);
-    float sk[2] = {ksc[0], ksc[1]}, sv[2] = {vsc[0], vsc[1]};
+    scales();
     __syncthreads();
     int buf = 0;
     for (int t0 = c0; t0 < c1; t0 += C::STEP) {
       const bool more = t0 + C::STEP < c1;
-      if (more) load(t0 + C::STEP);
+      if (more) {
+        load(t0 + C::STEP);
+        load_ids(t0 + 2 * C::STEP);
+      }
       if (t0 < lim_any) step(t0, smem + buf * C::STAGE, sk, sv);
       if (more) {
         stage(t0 + C::STEP, smem + (buf ^ 1) * C::STAGE);
-        sk[0] = ksc[0], sk[1] = ksc[1], sv[0] = vsc[0], sv[1] = vsc[1];
+        scales();
       }
       __syncthreads();
       buf ^= 1;

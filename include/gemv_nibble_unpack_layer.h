@@ -15,7 +15,7 @@
  *   v_codes  [num_pages, kv_heads, DP, page_size]   (values transposed: the
  *            attention kernel's matrix operand reads 16 tokens of a dim)
  *   k_scale, v_scale  float32 [num_pages, kv_heads]: one scale for each page
- *            of tokens and head; an element is code * scale.
+ *            of tokens and head, not negative; an element is code * scale.
  * DP is kv8_padded_dim(head_dim): head_dim rounded up to 64, 96, 128, 192 or
  * 256; the codes of dims past head_dim are zero (allocate the pool zeroed,
  * rope_append_kv8 writes zeros there). Codes are INT8 in [-127, 127] (W4_Q_I8)
