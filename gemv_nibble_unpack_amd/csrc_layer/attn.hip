@@ -383,7 +383,7 @@ __global__ __launch_bounds__(256) void k_attn_few(const AttnParams p) {
 // workspace they need.
 struct AttnPlan {
   bool many;                       // k_attn_many
-  int qt, tiles, chunk, splits, fold;
+  int qt, tiles, chunk, splits;
   int64_t units;
   size_t ws;
 };
@@ -393,18 +393,15 @@ inline AttnPlan attn_plan(int batch, int max_q, int max_kv, int group, int kv_he
   const int64_t rows = (int64_t)max_q * group;
   a.many = rows > 32;
   a.qt = rows > 16 ? 2 : 1;
-  const int tile = a.many ? MANY_ROWS : 16 * a.qt;
+  const int tile = a.many ? MANY_ROWS * (many_pair(dp) ? 2 : 1) : 16 * a.qt;
   a.tiles = (int)((rows + tile - 1) / tile);
   a.units = (int64_t)batch * kv_heads * a.tiles;
-  const int64_t least = a.many ? 512 : 256, blocks = a.many ? 448 : 1024;
+  const int64_t least = a.many ? 512 : 256, blocks = a.many ? 61440 / tile : 1024;
   int64_t splits = 1;
   if (a.units <= WS_COUNTER_SLOTS)
     splits = max((int64_t)1, min((max_kv + least - 1) / least, blocks / a.units));
   a.chunk = (int)(((max_kv + splits - 1) / splits + 255) / 256 * 256);
   a.splits = max(1, (max_kv + a.chunk - 1) / a.chunk);
-  // few enough blocks that all run at once (two a CU): the second half of the
-  // tiles in rising order, so that a CU's two blocks add up to the same work
-  a.fold = a.many && a.units * a.splits <= 512;
   a.ws = a.splits == 1 ? 0
                        : WS_COUNTERS + (size_t)a.units * a.splits * tile * (dp + (a.many ? 4 : 2)) * 4;
   return a;
@@ -434,7 +431,7 @@ using namespace w4;
 static bool attn_sizes_ok(int batch, int tokens, int max_q, int max_kv, int q_heads, int kv_heads,
                           int head_dim) {
   return batch >= 0 && tokens >= 0 && max_q >= 0 && max_kv >= 0 && max_kv <= (1 << 30) &&
-         kv_heads >= 1 && q_heads >= 1 && q_heads % kv_heads == 0 &&
+         kv_heads >= 1 && kv_heads < 65536 && q_heads >= 1 && q_heads % kv_heads == 0 &&
          kv8_padded_dim(head_dim) != 0 &&
          (int64_t)min(max_q, tokens) * (q_heads / kv_heads) <= 0x7fffffff / 2;
 }
@@ -485,7 +482,7 @@ extern "C" int paged_attn_kv8(const uint16_t* q, int64_t q_stride, const void* k
   p.batch = batch, p.tokens = tokens, p.max_kv = max_kv, p.cols = table_cols;
   p.q_heads = q_heads, p.kv_heads = kv_heads, p.group = q_heads / kv_heads, p.dim = head_dim;
   p.page_shift = __builtin_ctz(page_size), p.pages = num_pages;
-  p.tiles = a.tiles, p.chunk = a.chunk, p.splits = a.splits, p.fold = a.fold;
+  p.tiles = a.tiles, p.chunk = a.chunk, p.splits = a.splits;
   if (a.many) {
     if (a.units * a.splits > 0x7fffff) return W4_ERR_SHAPE;
     return launch_attn_many(p, dp, q_dtype, a.units * a.splits, stream);

@@ -21,12 +21,12 @@ struct AttnParams {
   int batch, tokens, max_q, max_kv, cols;
   int q_heads, kv_heads, group, dim;
   int page_shift, pages;
-  int tiles;                // row tiles of max_q * group rows
+  int tiles;                // row tiles (k_attn_many: blocks' worth of them) of max_q * group rows
   int chunk, splits;        // cached tokens per block (a multiple of 64), blocks along them
-  int fold;                 // many rows: order of the row tiles (see k_attn_many)
 };
 
-constexpr int MANY_ROWS = 128;    // query rows of a block of k_attn_many
+constexpr int MANY_ROWS = 128;    // query rows of a tile of k_attn_many
+constexpr bool many_pair(int dp) { return dp <= 128; }   // two tiles a block
 int launch_attn_many(const AttnParams& p, int dp, int kind, int64_t blocks, hipStream_t stream);
 
 // Sequence b's query rows and cached length. False: no new tokens, or ones
