@@ -388,7 +388,8 @@ struct AttnPlan {
   size_t ws;
 };
 
-inline AttnPlan attn_plan(int batch, int max_q, int max_kv, int group, int kv_heads, int dp) {
+inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int group, int kv_heads,
+                          int dp) {
   AttnPlan a{};
   const int64_t rows = (int64_t)max_q * group;
   a.many = rows > 32;
@@ -396,14 +397,32 @@ inline AttnPlan attn_plan(int batch, int max_q, int max_kv, int group, int kv_he
   const int tile = a.many ? MANY_ROWS * (many_pair(dp) ? 2 : 1) : 16 * a.qt;
   a.tiles = (int)((rows + tile - 1) / tile);
   a.units = (int64_t)batch * kv_heads * a.tiles;
-  const int64_t least = a.many ? 512 : 256, blocks = a.many ? 61440 / tile : 1024;
-  int64_t splits = 1;
-  if (a.units <= WS_COUNTER_SLOTS)
-    splits = max((int64_t)1, min((max_kv + least - 1) / least, blocks / a.units));
+  int64_t splits = 1, slots = a.units;
+  if (a.units <= WS_COUNTER_SLOTS) {
+    if (a.many) {
+      // blocks with work, at most: a ragged batch has fewer than its longest
+      // sequence's tiles times its size
+      slots = min(a.units, ((int64_t)tokens * group / tile + batch) * kv_heads);
+      const int64_t room = (W4_ATTN_WORKSPACE_MAX - WS_COUNTERS) / ((int64_t)tile * (dp + 4) * 4);
+      // One block a CU at a time. The number of chunks with the shortest run
+      // of whole rounds over the 256 CUs, a part's store and load costing as
+      // much as 65 tokens: 256 tokens of 32 heads over 16384 cached ones take
+      // 463 us unsplit, 99 us in 9 chunks; 2048 tokens over themselves (256
+      // blocks already) 55 us unsplit, 56 in 2.
+      const int64_t most = min((int64_t)((max_kv + 511) / 512), room / slots);
+      double best = 1e30;
+      for (int64_t s = 1; s <= max(most, (int64_t)1) && s <= 256; ++s) {
+        const double cost = (double)((slots * s + 255) / 256) / s + (s > 1 ? 65.0 * s / max_kv : 0.0);
+        if (cost < best) best = cost, splits = s;
+      }
+    } else {
+      splits = max((int64_t)1, min((int64_t)(max_kv + 255) / 256, 1024 / a.units));
+    }
+  }
   a.chunk = (int)(((max_kv + splits - 1) / splits + 255) / 256 * 256);
   a.splits = max(1, (max_kv + a.chunk - 1) / a.chunk);
   a.ws = a.splits == 1 ? 0
-                       : WS_COUNTERS + (size_t)a.units * a.splits * tile * (dp + (a.many ? 4 : 2)) * 4;
+                       : WS_COUNTERS + (size_t)slots * a.splits * tile * (dp + (a.many ? 4 : 2)) * 4;
   return a;
 }
 
@@ -440,7 +459,7 @@ extern "C" size_t paged_attn_kv8_workspace_bytes(int batch, int tokens, int max_
                                                  int q_heads, int kv_heads, int head_dim) {
   if (!attn_sizes_ok(batch, tokens, max_q, max_kv, q_heads, kv_heads, head_dim)) return 0;
   if (batch == 0 || tokens == 0 || max_q == 0) return 0;
-  return attn_plan(batch, min(max_q, tokens), max_kv, q_heads / kv_heads, kv_heads,
+  return attn_plan(batch, tokens, min(max_q, tokens), max_kv, q_heads / kv_heads, kv_heads,
                    kv8_padded_dim(head_dim)).ws;
 }
 
@@ -469,7 +488,7 @@ extern "C" int paged_attn_kv8(const uint16_t* q, int64_t q_stride, const void* k
   AttnParams p{};
   p.max_q = min(max_q, tokens);
   const int dp = kv8_padded_dim(head_dim);
-  const AttnPlan a = attn_plan(batch, p.max_q, max_kv, q_heads / kv_heads, kv_heads, dp);
+  const AttnPlan a = attn_plan(batch, tokens, p.max_q, max_kv, q_heads / kv_heads, kv_heads, dp);
   if (a.ws > 0 && (!workspace || workspace_bytes < a.ws)) return W4_ERR_WORKSPACE;
   p.q = q, p.q_stride = q_stride;
   p.kc = (const uint8_t*)k_codes, p.vc = (const uint8_t*)v_codes, p.ks = k_scale, p.vs = v_scale;
