@@ -1,14 +1,14 @@
 // Append of new keys and values to the paged 8-bit cache, with the position
 // rotation of queries and keys on the way.
 //
-// The scale of a page and head covers all its tokens, so the unit of work is
-// one (sequence, page, kv head) and one of three roles: the page's keys, its
-// values, or the queries of the same tokens (the heads that share the kv
-// head). A block finds the largest new magnitude, settles the page's scale,
-// re-codes the page's earlier tokens only if the scale grew, and codes the new
-// ones. The inputs are read twice (the second time from cache) instead of
-// being held, which keeps every page size and head dim in one kernel.
-// Bound: bytes (2 per element read, 1 written; queries 2 and 2).
+// The scale of a page and head covers all its tokens, so a block takes the new
+// tokens of one (sequence, page, kv head): it reads the keys and values into
+// registers, finds the largest magnitudes, settles the page's two scales,
+// re-codes the page's earlier tokens only where a scale grew, and writes the
+// codes. Other blocks turn the queries of the same tokens (the heads that
+// share the kv head). Bound: bytes (2 per element read, 1 written; queries 2
+// and 2); what costs beside them is a block's chain of dependent reads (lengths,
+// page number, scale), so the tokens are fetched beside that chain.
 //
 // Rotation: a' = a cos - b sin, b' = b cos + a sin with every product and sum
 // rounded (no contraction), so the codes do not depend on how a compiler
@@ -30,25 +30,24 @@ struct AppendParams {
   int batch, tokens, max_q, cols;
   int q_heads, kv_heads, dim, dp, page, pages;
   int columns;        // pages a sequence's new tokens can touch
-  int roles;          // 3, or 2 without queries
+  int q_span;         // kv heads whose queries one block turns
+  int q_blocks;       // blocks of queries per page (0 without queries)
 };
 
 // The new tokens of sequence b: first row, count, first position. False if
 // there are none or the lengths do not fit (see the header).
 __device__ __forceinline__ bool append_span(const AppendParams& p, int b, int& row, int& n,
                                             int& start) {
+  const int len = p.kv_len[b];                  // read beside q_indptr
   row = b;
   n = 1;
   if (p.indptr) {
     row = p.indptr[b];
-    const int end = p.indptr[b + 1];
-    if (row < 0 || end <= row || end > p.tokens) return false;
-    n = end - row;
+    n = p.indptr[b + 1] - row;
   }
-  const int len = p.kv_len[b];
   start = len - n;
-  return n <= p.max_q && start >= 0 && len <= (int64_t)p.cols * p.page &&
-         (p.rot == 0 || len <= p.rope_rows);
+  return row >= 0 && n > 0 && n <= p.tokens - row && n <= p.max_q && start >= 0 &&
+         len <= (int64_t)p.cols * p.page && (p.rot == 0 || len <= p.rope_rows);
 }
 
 template <typename T, int VEC>
@@ -62,51 +61,98 @@ __device__ __forceinline__ void load_vec(const T* p, float (&o)[VEC]) {
   }
 }
 
-// A head's elements as units of work: in the half layout the rot/2 / VEC
-// vectors of the first half, each with its partner in the second, then the
-// vectors that do not turn; in the interleaved layout every vector by itself.
-__device__ __forceinline__ int rope_units(int dim, int rot, int style, int vec) {
-  return (dim - (style == W4_ROPE_HALF ? rot / 2 : 0)) / vec;
+// A head's elements as units of two vectors: in the half layout a vector of
+// the first half with its partner in the second, then the dims that do not
+// turn, in pairs; in the interleaved layout all vectors, in pairs. An odd
+// vector at the end stands alone (d1 < 0).
+__host__ __device__ inline int rope_units(int dim, int rot, int style, int vec) {
+  const int turned = style == W4_ROPE_HALF ? rot / 2 / vec : 0;
+  return turned + ((dim - 2 * turned * vec) / vec + 1) / 2;
 }
-
-// Unit u of the head at x, turned by the table row cs: y0 at dim d0 and, if
-// d1 >= 0, y1 at dim d1.
-template <typename T, int VEC>
-__device__ __forceinline__ void rotated(const T* x, const float* cs, int u, int rot, int style,
-                                        float (&y0)[VEC], int& d0, float (&y1)[VEC], int& d1) {
-#pragma clang fp contract(off)
-  const int half = rot / 2;
+template <int VEC>
+__device__ __forceinline__ void unit_dims(int u, int dim, int rot, int style, int& d0, int& d1) {
+  const int half = style == W4_ROPE_HALF ? rot / 2 : 0;
   d0 = u * VEC;
-  d1 = -1;
-  if (style == W4_ROPE_HALF) {
-    if (d0 < half) {
-      d1 = d0 + half;
-      float a[VEC], b[VEC], c[VEC], s[VEC];
-      load_vec<T, VEC>(x + d0, a);
-      load_vec<T, VEC>(x + d1, b);
-      load_vec<float, VEC>(cs + d0, c);
-      load_vec<float, VEC>(cs + half + d0, s);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        y0[e] = a[e] * c[e] - b[e] * s[e];
-        y1[e] = b[e] * c[e] + a[e] * s[e];
-      }
-      return;
-    }
-    d0 += half;
-    load_vec<T, VEC>(x + d0, y0);
+  if (d0 < half) {
+    d1 = d0 + half;
     return;
   }
-  load_vec<T, VEC>(x + d0, y0);
-  if (d0 < rot) {
+  d0 += half;                                        // past the turned pairs
+  d1 = d0 + ((dim - 2 * half) / VEC + 1) / 2 * VEC;
+  if (d1 >= dim) d1 = -1;
+}
+template <int VEC>
+struct Unit {
+  float y0[VEC], y1[VEC];
+};
+template <typename T, int VEC>
+__device__ __forceinline__ Unit<VEC> load_unit(const T* x, int d0, int d1) {
+  Unit<VEC> y;
+  load_vec<T, VEC>(x + d0, y.y0);
+  load_vec<T, VEC>(x + (d1 >= 0 ? d1 : d0), y.y1);   // alone: the same vector twice
+  return y;
+}
+// the table's cosines and sines of a unit (row cs): of both vectors in the
+// interleaved layout, of the pair in the half layout; 1 and 0 for dims that do
+// not turn
+template <int VEC>
+struct Angle {
+  float c[VEC], s[VEC];
+};
+template <int VEC>
+__device__ __forceinline__ Angle<VEC> load_angle(const float* cs, int d0, int d1, int rot,
+                                                 int style) {
+  Angle<VEC> a;
+  const int half = rot / 2;
+  if (style == W4_ROPE_HALF) {
+    const bool in = d0 < half;
+    const float* t = cs + (in ? d0 : 0);
+    if (rot) {
+      load_vec<float, VEC>(t, a.c);
+      load_vec<float, VEC>(t + half, a.s);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      a.c[e] = in ? a.c[e] : 1.f;
+      a.s[e] = in ? a.s[e] : 0.f;
+    }
+    return a;
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {               // pairs of y0, then pairs of y1
+    const int d = (e < VEC / 2 ? d0 : d1 >= 0 ? d1 : d0) + 2 * (e % (VEC / 2));
+    const bool in = d < rot;
+    a.c[e] = in ? cs[d / 2] : 1.f;
+    a.s[e] = in ? cs[half + d / 2] : 0.f;
+  }
+  return a;
+}
+template <int VEC>
+__device__ __forceinline__ void turn_unit(Unit<VEC>& y, const Angle<VEC>& t, bool half, int d0,
+                                          int d1, int rot) {
+#pragma clang fp contract(off)
+  if (half) {
+    if (d0 >= rot / 2) return;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float a = y.y0[e], b = y.y1[e];
+      y.y0[e] = a * t.c[e] - b * t.s[e];
+      y.y1[e] = b * t.c[e] + a * t.s[e];
+    }
+    return;
+  }
+  auto one = [&](float (&v)[VEC], int d, int from) {
+    if (d >= rot) return;
 #pragma unroll
     for (int e = 0; e < VEC; e += 2) {
-      const float c = cs[(d0 + e) / 2], s = cs[half + (d0 + e) / 2];
-      const float a = y0[e], b = y0[e + 1];
-      y0[e] = a * c - b * s;
-      y0[e + 1] = b * c + a * s;
+      const float c = t.c[from + e / 2], s = t.s[from + e / 2];
+      const float a = v[e], b = v[e + 1];
+      v[e] = a * c - b * s;
+      v[e + 1] = b * c + a * s;
     }
-  }
+  };
+  one(y.y0, d0, 0);
+  one(y.y1, d1 >= 0 ? d1 : d0, VEC / 2);
 }
 
 // the scale for a largest magnitude m (bits), see the header
@@ -143,16 +189,18 @@ __device__ __forceinline__ uint32_t recoded(uint32_t w, float ratio) {
   return code4<Q>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
 }
 
-// img_row: bytes of one dim's staged values (at least the new tokens of a page)
-template <typename T, int Q, int VEC, int NT>
+// U: units a thread holds of a head's keys and of its values (a page's new
+// tokens are at most U * NT units). img_row: bytes of one dim's staged values.
+template <typename T, int Q, int VEC, int NT, int U>
 __global__ __launch_bounds__(NT) void k_rope_append(const AppendParams p, int img_row) {
   extern __shared__ __attribute__((aligned(16))) uint8_t img[];
-  __shared__ uint32_t shm[NT / 64];
+  __shared__ uint32_t shm[2][NT / 64];
+  // along one page: a block for each kv head, then blocks of q_span kv heads'
+  // queries
   int t = blockIdx.x;
-  const int h = t % p.kv_heads;
-  t /= p.kv_heads;
-  const int role = t % p.roles;
-  t /= p.roles;
+  const int per_page = p.kv_heads + p.q_blocks;
+  const int which = t % per_page;
+  t /= per_page;
   const int b = t / p.columns;
   const int j = t - b * p.columns;
   int row, n, start;
@@ -165,123 +213,189 @@ __global__ __launch_bounds__(NT) void k_rope_append(const AppendParams p, int im
   row += lo - start;                            // token row of position lo
   const int tid = threadIdx.x;
   const float* cs = p.rot ? p.rope + (size_t)lo * p.rot : nullptr;
+  const int nu = rope_units(D, p.rot, p.style, VEC);
 
-  if (role == 2) {                              // the queries of the heads on kv head h
-    const int G = p.q_heads / p.kv_heads;
-    const int nu = rope_units(D, p.rot, p.style, VEC);
-    const int per = G * nu;                     // units of one token
-    for (int i = tid; i < cnt * per; i += NT) {
-      const int tok = i / per, rem = i - tok * per;
-      const int g = rem / nu, u = rem - g * nu;
-      const int hh = h * G + g;
-      float y0[VEC], y1[VEC];
-      int d0, d1;
-      rotated<T, VEC>((const T*)p.q + (row + tok) * p.q_stride + (int64_t)hh * D,
-                      cs + (size_t)tok * p.rot, u, p.rot, p.style, y0, d0, y1, d1);
-      uint16_t* o = p.q_out + ((size_t)(row + tok) * p.q_heads + hh) * D;
-      auto put = [&](int d, const float (&y)[VEC]) {
-        if constexpr (VEC == 4)
-          *reinterpret_cast<u2*>(o + d) = __builtin_bit_cast(
-              u2, h4{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]});
-        else
-          *reinterpret_cast<h2*>(o + d) = h2{(_Float16)y[0], (_Float16)y[1]};
-      };
-      put(d0, y0);
-      if (d1 >= 0) put(d1, y1);
+  const bool half = p.style == W4_ROPE_HALF;
+  if (which >= p.kv_heads) {                    // queries
+    const int group = p.q_heads / p.kv_heads;
+    const int first = (which - p.kv_heads) * p.q_span * group;
+    const int per = min(p.q_span * group, p.q_heads - first) * nu;   // units of one token
+    const int all = cnt * per;
+    const bool few = all < (1 << 20);           // small_div's range
+    for (int i0 = tid; i0 < all; i0 += 2 * NT) {      // two at a time, read before either is stored
+      Unit<VEC> y[2];
+      int d0[2], d1[2];
+      size_t at[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int i = min(i0 + z * NT, all - 1);
+        const int tok = few ? small_div(i, per) : i / per;
+        const int rem = i - tok * per, g = few ? small_div(rem, nu) : rem / nu;
+        unit_dims<VEC>(rem - g * nu, D, p.rot, p.style, d0[z], d1[z]);
+        y[z] = load_unit<T, VEC>((const T*)p.q + (row + tok) * p.q_stride + (int64_t)(first + g) * D,
+                                 d0[z], d1[z]);
+        const Angle<VEC> a = load_angle<VEC>(cs + (size_t)tok * p.rot, d0[z], d1[z], p.rot, p.style);
+        turn_unit<VEC>(y[z], a, half, d0[z], d1[z], p.rot);
+        at[z] = ((size_t)(row + tok) * p.q_heads + first + g) * D;
+      }
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        if (i0 + z * NT >= all) break;
+        auto put = [&](int d, const float (&v)[VEC]) {
+          uint16_t* o = p.q_out + at[z] + d;
+          if constexpr (VEC == 4)
+            *reinterpret_cast<u2*>(o) = __builtin_bit_cast(
+                u2, h4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]});
+          else
+            *reinterpret_cast<h2*>(o) = h2{(_Float16)v[0], (_Float16)v[1]};
+        };
+        put(d0[z], y[z].y0);
+        if (d1[z] >= 0) put(d1[z], y[z].y1);
+      }
     }
     return;
   }
 
-  const int id = p.table[(size_t)b * p.cols + col];
-  if (id < 0 || id >= p.pages) return;
-  const bool keys = role == 0;
-  const size_t ph = (size_t)id * p.kv_heads + h;
-  float* sc = (keys ? p.ks : p.vs) + ph;
-  uint8_t* codes = (keys ? p.kc : p.vc) + ph * P * DP;
-  const T* src = keys ? (const T*)p.k + row * p.k_stride + (int64_t)h * D
-                      : (const T*)p.v + row * p.v_stride + (int64_t)h * D;
-  const int64_t stride = keys ? p.k_stride : p.v_stride;
-  const int rot = keys ? p.rot : 0;
-  const int nu = rope_units(D, rot, p.style, VEC);
+  const int h = which;
+  // ---- the new keys and values ------------------------------------------------
+  const int nv = rope_units(D, 0, W4_ROPE_INTERLEAVED, VEC);
+  Unit<VEC> ky[U], vy[U];
+  Angle<VEC> ang[U];
+  // unit i = tid + z * NT of a head's keys: token, dims (threads past the end
+  // repeat the last unit and store nothing)
+  auto kunit = [&](int z, int& tok, int& d0, int& d1) {
+    const int i = min(tid + z * NT, cnt * nu - 1);
+    tok = small_div(i, nu);
+    unit_dims<VEC>(i - tok * nu, D, p.rot, p.style, d0, d1);
+    return tid + z * NT < cnt * nu;
+  };
+  auto vunit = [&](int z, int& tok, int& d0, int& d1) {
+    const int i = min(tid + z * NT, cnt * nv - 1);
+    tok = small_div(i, nv);
+    unit_dims<VEC>(i - tok * nv, D, 0, W4_ROPE_INTERLEAVED, d0, d1);
+    return tid + z * NT < cnt * nv;
+  };
+#pragma unroll
+  for (int z = 0; z < U; ++z) {
+    int kt, k0, k1, vt, v0, v1;
+    kunit(z, kt, k0, k1);
+    vunit(z, vt, v0, v1);
+    ang[z] = load_angle<VEC>(cs + (size_t)kt * p.rot, k0, k1, p.rot, p.style);
+    ky[z] = load_unit<T, VEC>((const T*)p.k + (row + kt) * p.k_stride + (int64_t)h * D, k0, k1);
+    vy[z] = load_unit<T, VEC>((const T*)p.v + (row + vt) * p.v_stride + (int64_t)h * D, v0, v1);
+  }
+  // a page outside the pool: the block goes on without storing
+  const int idt = p.table[(size_t)b * p.cols + col];
+  const bool store = idt >= 0 && idt < p.pages;
+  const int id = store ? idt : 0;
   const int lead = lo - col * P;                // earlier tokens of the page
-  const float old = lead > 0 ? *sc : 0.f;
+  const size_t ph = (size_t)id * p.kv_heads + h;
+  float kold = p.ks[ph], vold = p.vs[ph];
 
-  // ---- the page's scale -----------------------------------------------------
-  uint32_t mx = 0;
-  for (int i = tid; i < cnt * nu; i += NT) {
-    const int tok = i / nu;
-    float y0[VEC], y1[VEC];
-    int d0, d1;
-    rotated<T, VEC>(src + tok * stride, cs + (size_t)tok * p.rot, i - tok * nu, rot, p.style, y0,
-                    d0, y1, d1);
+  // ---- the page's scales --------------------------------------------------------
+  uint32_t km = 0, vm = 0;
+#pragma unroll
+  for (int z = 0; z < U; ++z) {
+    int tok, d0, d1;
+    kunit(z, tok, d0, d1);
+    turn_unit<VEC>(ky[z], ang[z], half, d0, d1, p.rot);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      mx = max(mx, abs_bits(y0[e]));
-      if (d1 >= 0) mx = max(mx, abs_bits(y1[e]));
+      km = max(km, max(abs_bits(ky[z].y0[e]), abs_bits(ky[z].y1[e])));
+      vm = max(vm, max(abs_bits(vy[z].y0[e]), abs_bits(vy[z].y1[e])));
     }
   }
-  mx = wave_max_u(mx);
+  km = wave_max_u(km);
+  vm = wave_max_u(vm);
   if constexpr (NT > 64) {
-    if ((tid & 63) == 0) shm[tid >> 6] = mx;
+    if ((tid & 63) == 0) {
+      shm[0][tid >> 6] = km;
+      shm[1][tid >> 6] = vm;
+    }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NT / 64; ++i) mx = max(mx, shm[i]);
+    for (int i = 0; i < NT / 64; ++i) {
+      km = max(km, shm[0][i]);
+      vm = max(vm, shm[1][i]);
+    }
   }
+  if (lead == 0) kold = vold = 0.f;
   // max of magnitudes by their bits: a NaN of either side wins
-  const float s = __uint_as_float(max(__float_as_uint(scale_for<Q>(mx)), abs_bits(old)));
-  if (tid == 0) *sc = s;
-  const bool grown = lead > 0 && old < s;       // false if either is NaN
-  const float ratio = grown ? old / s : 1.f;
+  const float ks = __uint_as_float(max(__float_as_uint(scale_for<Q>(km)), abs_bits(kold)));
+  const float vs = __uint_as_float(max(__float_as_uint(scale_for<Q>(vm)), abs_bits(vold)));
+  if (!store) return;
+  if (tid == 0) {
+    p.ks[ph] = ks;
+    p.vs[ph] = vs;
+  }
 
-  if (keys) {
-    // earlier slots, the new ones, their padding, and a begun page's rest
-    if (grown) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(codes);
+  // ---- keys: earlier slots, the new ones, their padding, a begun page's rest -----
+  const int pad = (DP - D) / 4;
+  {
+    uint8_t* kc = p.kc + ph * P * DP;
+    if (lead > 0 && kold < ks) {              // grown (false for NaN)
+      const float ratio = kold / ks;
+      uint32_t* w = reinterpret_cast<uint32_t*>(kc);
       for (int i = tid; i < lead * (DP / 4); i += NT) w[i] = recoded<Q>(w[i], ratio);
     }
-    uint8_t* dst = codes + (size_t)lead * DP;
-    for (int i = tid; i < cnt * nu; i += NT) {
-      const int tok = i / nu;
-      float y0[VEC], y1[VEC];
-      int d0, d1;
-      rotated<T, VEC>(src + tok * stride, cs + (size_t)tok * p.rot, i - tok * nu, rot, p.style, y0,
-                      d0, y1, d1);
-      put_codes<VEC>(dst + tok * DP + d0, codes_of<Q, VEC>(y0, s));
-      if (d1 >= 0) put_codes<VEC>(dst + tok * DP + d1, codes_of<Q, VEC>(y1, s));
+    uint8_t* dst = kc + (size_t)lead * DP;
+#pragma unroll
+    for (int z = 0; z < U; ++z) {
+      int tok, d0, d1;
+      if (kunit(z, tok, d0, d1)) {
+        put_codes<VEC>(dst + tok * DP + d0, codes_of<Q, VEC>(ky[z].y0, ks));
+        if (d1 >= 0) put_codes<VEC>(dst + tok * DP + d1, codes_of<Q, VEC>(ky[z].y1, ks));
+      }
+      if (vunit(z, tok, d0, d1)) {                  // values, staged as [dim][new token]
+        const uint32_t w0 = codes_of<Q, VEC>(vy[z].y0, vs);
+        const uint32_t w1 = codes_of<Q, VEC>(vy[z].y1, vs);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          img[(d0 + e) * img_row + tok] = (uint8_t)(w0 >> (8 * e));
+          if (d1 >= 0) img[(d1 + e) * img_row + tok] = (uint8_t)(w1 >> (8 * e));
+        }
+      }
     }
-    const int pad = (DP - D) / 4;
     for (int i = tid; i < cnt * pad; i += NT) {
-      const int tok = i / pad;
+      const int tok = small_div(i, pad);
       *reinterpret_cast<uint32_t*>(dst + tok * DP + D + 4 * (i - tok * pad)) = 0u;
     }
     if (lead == 0) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(codes + (size_t)cnt * DP);
+      uint32_t* w = reinterpret_cast<uint32_t*>(kc + (size_t)cnt * DP);
       for (int i = tid; i < (P - cnt) * (DP / 4); i += NT) w[i] = 0u;
     }
-    return;
-  }
-
-  // ---- values: codes staged as [dim][new token], written as rows of slots -----
-  for (int i = tid; i < cnt * nu; i += NT) {
-    const int tok = i / nu, d = (i - tok * nu) * VEC;
-    float y[VEC];
-    load_vec<T, VEC>(src + tok * stride + d, y);
-    const uint32_t w = codes_of<Q, VEC>(y, s);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) img[(d + e) * img_row + tok] = (uint8_t)(w >> (8 * e));
   }
   __syncthreads();
-  // words of four slots that change: every word of a begun page, otherwise
-  // those up to the last new token, from the first one if the scale grew
-  const int w0 = lead == 0 || grown ? 0 : lead / 4;
-  const int w1 = lead == 0 ? P / 4 : (lead + cnt + 3) / 4;
-  const int nw = w1 - w0;
-  for (int i = tid; i < DP * nw; i += NT) {
-    const int d = i / nw, slot = 4 * (w0 + i - d * nw);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(codes + (size_t)d * P + slot);
-    uint32_t w = 0;
-    if (lead > 0) {
-      w = *dst;
+  // ---- values: rows of slots --------------------------------------------------------
+  {
+    uint8_t* vc = p.vc + ph * P * DP;
+    if (lead == 0) {
+      // the whole page, 16 slots at a time; staged rows are words
+      const int sh = __builtin_ctz(P) - 4;
+      for (int i = tid; i < DP << sh; i += NT) {
+        const int d = i >> sh, slot = 16 * (i - (d << sh));
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(img + d * img_row + slot);
+        u4 w;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int left = min(max(cnt - slot - 4 * x, 0), 4);   // new tokens of the word
+          w[x] = d >= D || left == 0 ? 0u
+                                     : src[x] & (left == 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1u);
+        }
+        *reinterpret_cast<u4*>(vc + (size_t)d * P + slot) = w;
+      }
+      return;
+    }
+    // words of four slots that change: those of the new tokens, from the first
+    // one if the scale grew
+    const bool grown = vold < vs;
+    const float ratio = grown ? vold / vs : 1.f;
+    const int w0 = grown ? 0 : lead / 4;
+    const int nw = (lead + cnt + 3) / 4 - w0;
+    for (int i = tid; i < DP * nw; i += NT) {
+      const int d = small_div(i, nw), slot = 4 * (w0 + i - d * nw);
+      uint32_t* at = reinterpret_cast<uint32_t*>(vc + (size_t)d * P + slot);
+      uint32_t w = *at;
       if (grown) {
         const uint32_t r = recoded<Q>(w, ratio);
         // slots from `lead` on are not earlier tokens: left as they are
@@ -289,38 +403,53 @@ __global__ __launch_bounds__(NT) void k_rope_append(const AppendParams p, int im
         const uint32_t m = before == 4 ? 0xFFFFFFFFu : (1u << (8 * before)) - 1u;
         w = (r & m) | (w & ~m);
       }
-    }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int tok = slot + e - lead;
-      if (tok >= 0 && tok < cnt) {
-        const uint32_t c = d < D ? img[d * img_row + tok] : 0u;
-        w = (w & ~(0xFFu << (8 * e))) | (c << (8 * e));
+      for (int e = 0; e < 4; ++e) {
+        const int tok = slot + e - lead;
+        if (tok >= 0 && tok < cnt) {
+          const uint32_t c = d < D ? img[d * img_row + tok] : 0u;
+          w = (w & ~(0xFFu << (8 * e))) | (c << (8 * e));
+        }
       }
+      *at = w;
     }
-    *dst = w;
   }
 }
 
 template <typename T, int Q>
-int launch_append(const AppendParams& p, hipStream_t stream) {
-  const int64_t blocks = (int64_t)p.batch * p.columns * p.roles * p.kv_heads;
-  if (blocks > 0x7fffff) return W4_ERR_SHAPE;    // 2^31 threads
+int launch_append(AppendParams& p, hipStream_t stream) {
   // vectors of four lie on one side of every pair: half layout rot/2 a
   // multiple of 4 (rot is a multiple of 4 in either layout)
   const bool v4 = p.style == W4_ROPE_INTERLEAVED || p.rot % 8 == 0;
-  const int img_row = (min(p.page, p.max_q) + 3) / 4 * 4 + 4;
-  const size_t lds = (size_t)p.dp * img_row;
-  const bool one = p.max_q == 1;
-#define W4_AP(VEC, NT)                                                                             \
-  hipLaunchKernelGGL((k_rope_append<T, Q, VEC, NT>), dim3((unsigned)blocks), dim3(NT), lds, stream, \
-                     p, img_row)
-  if (one) {
-    if (v4) W4_AP(4, 64);
-    else W4_AP(2, 64);
+  const int slots = min(p.page, p.max_q);
+  // bytes of a staged row: words, one more than the slots need, which keeps the
+  // rows of neighbouring dims off one bank
+  const int img_row = (slots + 3) / 4 * 4 + 4;
+  const int vec = v4 ? 4 : 2;
+  const int units = slots * max(rope_units(p.dim, p.rot, p.style, vec),
+                                rope_units(p.dim, 0, W4_ROPE_INTERLEAVED, vec));
+  const int64_t per_head = (int64_t)slots * (p.q_heads / p.kv_heads) *
+                           rope_units(p.dim, p.rot, p.style, vec);
+#define W4_AP(VEC, NT, U)                                                                       \
+  do {                                                                                          \
+    /* queries of as many kv heads as give each thread four units */                            \
+    p.q_span = (int)max((int64_t)1, min((int64_t)p.kv_heads, 4 * NT / per_head));               \
+    p.q_blocks = p.q ? (p.kv_heads + p.q_span - 1) / p.q_span : 0;                              \
+    const int64_t blocks = (int64_t)p.batch * p.columns * (p.kv_heads + p.q_blocks);            \
+    if (blocks * NT > 0x7fffffff) return W4_ERR_SHAPE;                                          \
+    hipLaunchKernelGGL((k_rope_append<T, Q, VEC, NT, U>), dim3((unsigned)blocks), dim3(NT),     \
+                       (size_t)p.dp * img_row + 16, stream, p, img_row);                        \
+  } while (0)
+  if (v4) {
+    if (units <= 64) W4_AP(4, 64, 1);
+    else if (units <= 256) W4_AP(4, 256, 1);
+    else if (units <= 1024) W4_AP(4, 512, 2);
+    else W4_AP(4, 1024, 4);
   } else {
-    if (v4) W4_AP(4, 256);
-    else W4_AP(2, 256);
+    if (units <= 128) W4_AP(2, 64, 2);
+    else if (units <= 512) W4_AP(2, 256, 2);
+    else if (units <= 2048) W4_AP(2, 512, 4);
+    else W4_AP(2, 1024, 8);
   }
 #undef W4_AP
   return launch_status();
@@ -378,7 +507,6 @@ extern "C" int rope_append_kv8(const void* q, const void* k, const void* v, int 
   p.q_heads = q_heads, p.kv_heads = kv_heads, p.dim = head_dim, p.dp = dp;
   p.page = page_size, p.pages = num_pages;
   p.columns = (p.max_q + page_size - 2) / page_size + 1;
-  p.roles = q ? 3 : 2;
   if (in_dtype == W4_IN_F16)
     return q_dtype == W4_Q_I8 ? launch_append<uint16_t, W4_Q_I8>(p, stream)
                               : launch_append<uint16_t, W4_Q_F8>(p, stream);
