@@ -52,10 +52,12 @@ struct KVRegs {
   u2 kr[4];
   u4 v[DP / 16];
   float ks, vs;
+  uint32_t bad;
 };
 
+// two blocks a CU where their registers allow it
 template <int DP, int Q, int QT>
-__global__ __launch_bounds__(256) void k_attn_few(const AttnParams p) {
+__global__ __launch_bounds__(256, DP < 256 && DP * QT <= 256 ? 2 : 1) void k_attn_few(const AttnParams p) {
   using C = AttnFew<DP, Q, QT>;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   float* so = reinterpret_cast<float*>(smem);                       // [4][ROWS][OROW]
@@ -119,31 +121,49 @@ __global__ __launch_bounds__(256) void k_attn_few(const AttnParams p) {
   const int c0 = split * p.chunk;
   const int c1 = min(seen, c0 + p.chunk);
   const int last16 = (max(seen, 1) - 1) & ~15;      // start of the last group with a token
-  const size_t kpage = (size_t)p.kv_heads << p.page_shift;   // rows per page
+  const uint32_t page_bytes = (uint32_t)p.kv_heads * DP << p.page_shift;
+  const uint8_t* khead = p.kc + ((int64_t)h * DP << p.page_shift);
+  const uint8_t* vhead = p.vc + ((int64_t)h * DP << p.page_shift);
 
-  // Step at token t: group of tokens of K operand row c and of row g
-  auto load = [&](int t0, KVRegs<DP>& r) {
-    const int tk = min(t0 + 16 * (c >> 2), last16), tv = min(t0 + 16 * g, last16);
-    int ik = tab[tk >> p.page_shift], iv = tab[tv >> p.page_shift];
-    const bool okv = iv >= 0 && iv < p.pages;
-    ik = ik >= 0 && ik < p.pages ? ik : 0;
-    iv = okv ? iv : 0;
-    const size_t sv = (size_t)iv * p.kv_heads + h;
-    r.ks = okv ? p.ks[sv] : __uint_as_float(0x7FC00000u);
-    r.vs = p.vs[sv];
-    const uint8_t* kp = p.kc + ((size_t)ik * kpage + ((size_t)h << p.page_shift) +
-                                (tk & (P - 1)) + (c & 3)) * DP;
-    const uint8_t* vp = p.vc + (((size_t)iv * p.kv_heads + h) * DP + c) * P + (tv & (P - 1));
+  // A step's codes into registers: K operand row c takes tokens of group c >> 2,
+  // this lane's own tokens are group g. The next step's keys are fetched as
+  // soon as the first product has taken this one's, the values after the
+  // second, so the same registers serve; page numbers are fetched one step
+  // before. All loads go out before the work that follows in the program.
+  KVRegs<DP> r;
+  int ikn, ivn;                                     // page numbers of the next loads
+  auto load_ids = [&](int t0) {
+    ikn = tab[min(t0 + 16 * (c >> 2), last16) >> p.page_shift];
+    ivn = tab[min(t0 + 16 * g, last16) >> p.page_shift];
+  };
+  auto load_k = [&](int t0) {
+    const int tk = min(t0 + 16 * (c >> 2), last16);
+    const uint32_t ik = ikn >= 0 && ikn < p.pages ? ikn : 0;
+    const uint8_t* kp = khead + (uint64_t)ik * page_bytes + ((tk & (P - 1)) + (c & 3)) * DP + 16 * g;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int s = 0; s < C::KH; ++s)
-        r.k[i][s] = *reinterpret_cast<const u4*>(kp + 4 * i * DP + 64 * s + 16 * g);
+        r.k[i][s] = *reinterpret_cast<const u4*>(kp + 4 * i * DP + 64 * s);
       if constexpr (C::KR)
-        r.kr[i] = *reinterpret_cast<const u2*>(kp + 4 * i * DP + 64 * C::KH + 8 * g);
+        r.kr[i] = *reinterpret_cast<const u2*>(kp + 4 * i * DP + 64 * C::KH - 8 * g);
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto load_v = [&](int t0) {
+    const int tv = min(t0 + 16 * g, last16);
+    const bool ok = ivn >= 0 && ivn < p.pages;
+    const uint32_t iv = ok ? ivn : 0;
+    load_ids(t0 + 256);
+    r.bad = ok ? 0u : 0x7FC00000u;                   // a page outside the pool: its key scale is NaN
+    const uint64_t at = (uint64_t)iv * (uint32_t)p.kv_heads + h;
+    r.ks = p.ks[at];
+    r.vs = p.vs[at];
+    const uint8_t* vp = vhead + (uint64_t)iv * page_bytes + (c << p.page_shift) + (tv & (P - 1));
 #pragma unroll
-    for (int d = 0; d < C::DT; ++d) r.v[d] = *reinterpret_cast<const u4*>(vp + (size_t)16 * d * P);
+    for (int d = 0; d < C::DT; ++d)
+      r.v[d] = *reinterpret_cast<const u4*>(vp + ((16 * d) << p.page_shift));
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   f4 o[QT][C::DT];
@@ -157,7 +177,7 @@ __global__ __launch_bounds__(256) void k_attn_few(const AttnParams p) {
     for (int d = 0; d < C::DT; ++d) o[u][d] = f4{0.f, 0.f, 0.f, 0.f};
   }
 
-  auto step = [&](int t0, KVRegs<DP>& r) {
+  auto step = [&](int t0, bool more) {
     f4 s[QT][4];
 #pragma unroll
     for (int u = 0; u < QT; ++u)
@@ -182,8 +202,9 @@ __global__ __launch_bounds__(256) void k_attn_few(const AttnParams p) {
           s[u][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[u][C::KS - 1], s[u][i], 0, 0, 0);
       }
     }
+    if (more) load_k(t0 + 256);
     const int tg = t0 + 16 * g;                     // this lane's 16 tokens
-    const float a = r.ks * p.scale_log2;
+    const float a = __uint_as_float(__float_as_uint(r.ks) | r.bad) * p.scale_log2;
     // a lane without a token in reach may hold any scale: it counts as none
     const float vs = tg < c1 ? r.vs : 0.f;
     const float nref = fmaxf(ref, rows_max(vs));
@@ -249,14 +270,15 @@ __global__ __launch_bounds__(256) void k_attn_few(const AttnParams p) {
         o[u][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w[u][1], o[u][d], 0, 0, 0);
       }
     }
+    if (more) load_v(t0 + 256);
   };
 
-  {
-    KVRegs<DP> r;
-    for (int t0 = c0 + 64 * wave; t0 < c1; t0 += 256) {
-      load(t0, r);
-      step(t0, r);
-    }
+  if (c0 + 64 * wave < c1) {
+    int t0 = c0 + 64 * wave;
+    load_ids(t0);
+    load_k(t0);
+    load_v(t0);
+    for (; t0 < c1; t0 += 256) step(t0, t0 + 256 < c1);
   }
 
   // ---- the four waves' results to LDS ---------------------------------------
@@ -346,36 +368,64 @@ __global__ __launch_bounds__(256) void k_attn_few(const AttnParams p) {
   __syncthreads();
   if (!*slast) return;
   if (tid == 0) dev_store(p.counters + unit, 0u);
-  for (int i = tid; i < nr * NV; i += 256) {
-    const int r = i / NV, d = 4 * (i % NV);
+  // Items are (row, 4 dims); where they leave threads idle, 2, 4 or 8 threads
+  // share an item's parts. Eight parts' loads are issued together: each is a
+  // round trip to the level that all XCDs share, and one after another they
+  // took longer than the block's own share of the tokens.
+  const int items = nr * NV;
+  const int share = items <= 32 ? 8 : items <= 64 ? 4 : items <= 128 ? 2 : 1;
+  float* sj = so;                                   // [share][items][6]
+  for (int i0 = 0; i0 < items; i0 += 256 / share) {
+    const int lane_item = tid & (256 / share - 1), pg = tid / (256 / share);
+    const int i = min(i0 + lane_item, items - 1);
+    const int rr = i / NV, d = 4 * (i % NV);
     float M = -__builtin_inff(), L = 0.f;
     f4 s = {0.f, 0.f, 0.f, 0.f};
-    // parts four at a time, their loads issued together
-    for (int z = 0; z < parts; z += 4) {
-      uint64_t ml[4], a[4], e2[4];
+    for (int z = pg; z < parts; z += 8 * share) {
+      uint64_t ml[8], x[8], y[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t* q = po + min(z + k, parts - 1) * pstride;
-        ml[k] = dev_load2(q + C::ROWS * DP + 2 * r);
-        a[k] = dev_load2(q + r * DP + d);
-        e2[k] = dev_load2(q + r * DP + d + 2);
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t* q = po + min(z + k * share, parts - 1) * pstride;
+        ml[k] = dev_load2(q + C::ROWS * DP + 2 * rr);
+        x[k] = dev_load2(q + rr * DP + d);
+        y[k] = dev_load2(q + rr * DP + d + 2);
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (z + k >= parts) break;
+      for (int k = 0; k < 8; ++k) {
+        if (z + k * share >= parts) break;
         const float Mk = __uint_as_float((uint32_t)ml[k]), Lk = __uint_as_float(ml[k] >> 32);
         const float nm = fmaxf(M, Mk);
         const float base = nm == -__builtin_inff() ? 0.f : nm;
         const float fo = __builtin_amdgcn_exp2f(M - base), fn = __builtin_amdgcn_exp2f(Mk - base);
         M = nm;
         L = L * fo + Lk * fn;
-        s[0] = s[0] * fo + __uint_as_float((uint32_t)a[k]) * fn;
-        s[1] = s[1] * fo + __uint_as_float((uint32_t)(a[k] >> 32)) * fn;
-        s[2] = s[2] * fo + __uint_as_float((uint32_t)e2[k]) * fn;
-        s[3] = s[3] * fo + __uint_as_float((uint32_t)(e2[k] >> 32)) * fn;
+        s[0] = s[0] * fo + __uint_as_float((uint32_t)x[k]) * fn;
+        s[1] = s[1] * fo + __uint_as_float((uint32_t)(x[k] >> 32)) * fn;
+        s[2] = s[2] * fo + __uint_as_float((uint32_t)y[k]) * fn;
+        s[3] = s[3] * fo + __uint_as_float((uint32_t)(y[k] >> 32)) * fn;
       }
     }
-    finish(r, d, M, L, s);
+    if (share > 1) {                                // uniform; one pass over the items then
+      float* q = sj + (pg * items + i) * 6;
+      if (lane_item < items) {
+        q[0] = M, q[1] = L;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[2 + e] = s[e];
+      }
+      __syncthreads();
+      if (pg != 0 || lane_item >= items) return;
+      for (int g2 = 1; g2 < share; ++g2) {
+        const float* w = sj + (g2 * items + i) * 6;
+        const float nm = fmaxf(M, w[0]);
+        const float base = nm == -__builtin_inff() ? 0.f : nm;
+        const float fo = __builtin_amdgcn_exp2f(M - base), fn = __builtin_amdgcn_exp2f(w[0] - base);
+        M = nm;
+        L = L * fo + w[1] * fn;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = s[e] * fo + w[2 + e] * fn;
+      }
+    }
+    if (i0 + lane_item < items) finish(rr, d, M, L, s);
   }
 }
 
@@ -397,6 +447,7 @@ inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int grou
   const int tile = a.many ? MANY_ROWS * (many_pair(dp) ? 2 : 1) : 16 * a.qt;
   a.tiles = (int)((rows + tile - 1) / tile);
   a.units = (int64_t)batch * kv_heads * a.tiles;
+  constexpr int least = 256;
   int64_t splits = 1, slots = a.units;
   if (a.units <= WS_COUNTER_SLOTS) {
     if (a.many) {
@@ -416,10 +467,17 @@ inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int grou
         if (cost < best) best = cost, splits = s;
       }
     } else {
-      splits = max((int64_t)1, min((int64_t)(max_kv + 255) / 256, 1024 / a.units));
+      // About one round of the 512 resident blocks: one token of 8 kv heads
+      // over 131072 cached ones takes 56 us in 64 chunks, 60 in 96, 63 in
+      // 128. A batch's lengths are mostly below their bound and leave blocks
+      // without work: 32 sequences of 1 to 4096 tokens take 34 us in 3 chunks,
+      // 38 in 2. Chunks of 256 tokens (one step a wave) or more.
+      const int64_t target = batch > 1 ? 640 : 512;
+      splits = max((int64_t)1, min((int64_t)(max_kv + least - 1) / least,
+                                   (target + a.units / 2) / a.units));
     }
   }
-  a.chunk = (int)(((max_kv + splits - 1) / splits + 255) / 256 * 256);
+  a.chunk = (int)(((max_kv + splits - 1) / splits + least - 1) / least * least);
   a.splits = max(1, (max_kv + a.chunk - 1) / a.chunk);
   a.ws = a.splits == 1 ? 0
                        : WS_COUNTERS + (size_t)slots * a.splits * tile * (dp + (a.many ? 4 : 2)) * 4;
