@@ -46,7 +46,7 @@ __device__ __forceinline__ bool append_span(const AppendParams& p, int b, int& r
     n = p.indptr[b + 1] - row;
   }
   start = len - n;
-  return row >= 0 && n > 0 && n <= p.tokens - row && n <= p.max_q && start >= 0 &&
+  return row >= 0 && n > 0 && n <= p.tokens - row && n <= p.max_q && len >= n &&
          len <= (int64_t)p.cols * p.page && (p.rot == 0 || len <= p.rope_rows);
 }
 

@@ -161,6 +161,7 @@ int launch_norm(const void* X, const void* R, const void* Wt, int M, int K, floa
   if (K <= 1024) W4_NORM(1, 2);
   else if (K <= 4096) W4_NORM(4, 2);
   else if (K <= 8192) W4_NORM(8, 2);
+  else if (K <= 12288) W4_NORM(8, 3);      // 333 float32 rows of 8640: 4.9 us; 16 waves x 2 6.0, 4 x 5 5.3
   else if (K <= 16384) W4_NORM(16, 2);
   else W4_NORM(16, 0);
 #undef W4_NORM

@@ -349,6 +349,24 @@ def test_append_skips_what_does_not_fit(g):
     assert np.array_equal(host(q_out), want)
 
 
+def test_append_extreme_lengths(g):
+    """Lengths and offsets at the ends of their type are refused by the kernel itself."""
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    cdev = g.kv8_alloc(4, 16, 1, 64)
+    x = dev(np.ones((5, 1, 64), np.float16))
+    before = [t.clone() for t in cdev]
+    q_out = torch.full((5, 1, 64), 7.0, dtype=torch.float16, device="cuda")
+    table = dev(np.zeros((1, 2), np.int32))
+    for n in (lo, lo + 4, -1, hi):
+        for ip in ([0, 5], [0, hi], [lo, 5], [3, lo], [hi, lo]):
+            g.rope_append_kv8(x, x, x, *cdev, table, dev(np.array([n], np.int32)),
+                              q_indptr=dev(np.array(ip, np.int64).astype(np.int32)), max_q=5,
+                              q_out=q_out)
+    for a, b in zip(before, cdev):
+        assert torch.equal(a, b)
+    assert (host(q_out) == 7.0).all()
+
+
 # ------------------------------------------------------------------ attention
 def random_cache(rng, lens, page, Hkv, D, dp, kind, spread=1.0):
     table, pool = page_tables(rng, lens, page)
@@ -550,6 +568,41 @@ def test_attention_lengths_that_do_not_fit(g):
     out = host(g.paged_attn_kv8(q, *cd, kv, 20, q_indptr=dev(np.array([0, 3, 4, 2, 9], np.int32)),
                                 max_q=2, out=keep))
     assert np.isnan(out[:2]).all() and (out[2] == 5.0).all() and np.isfinite(out[3]).all()
+
+
+@pytest.mark.parametrize("max_q", [5, 100])
+def test_attention_extreme_lengths(g, max_q):
+    rng = np.random.default_rng(37)
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    cache, table = random_cache(rng, [20], 16, 1, 64, 64, 1)
+    cd = (device_codes(cache, 0), device_codes(cache, 1), dev(cache.scale[0]), dev(cache.scale[1]),
+          dev(table))
+    q = dev(np.ones((5, 1, 64), np.float16))
+    for n in (lo, -1, hi):
+        out = host(g.paged_attn_kv8(q, *cd, dev(np.array([n], np.int32)), 20,
+                                    q_indptr=dev(np.array([0, 5], np.int32)), max_q=max_q))
+        assert np.isnan(out).all()
+    for ip in ([0, hi], [lo, 5], [3, lo], [hi, lo], [4, 4]):
+        keep = torch.full((5, 1, 64), 5.0, dtype=torch.float16, device="cuda")
+        g.paged_attn_kv8(q, *cd, dev(np.array([20], np.int32)), 20, max_q=max_q, out=keep,
+                         q_indptr=dev(np.array(ip, np.int64).astype(np.int32)))
+        assert (host(keep) == 5.0).all(), ip
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("n", [33, 129, 300])
+def test_attention_many_rows_split(g, kind, n):
+    """Chunks of long contexts: row tiles alone and in pairs, split over blocks."""
+    rng = np.random.default_rng(38)
+    lens = [5000, 2600, n]
+    cache, table = random_cache(rng, lens, 32, 1, 128, 128, kind)
+    spoil_past_end(cache, table, lens)
+    assert g.paged_attn_kv8_workspace_bytes(3, n + 40, n, 5000, 1, 1, 128) > 0
+    _, w = check_attention(g, rng, cache, table, lens, [n, 35, 5], 1)
+    say("split", kind, n, "worst share of the bound", round(w, 3))
+    a, _ = check_attention(g, np.random.default_rng(1), cache, table, lens, [n, 35, 5], 1)
+    b, _ = check_attention(g, np.random.default_rng(1), cache, table, lens, [n, 35, 5], 1)
+    assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("n", [1, 4])
