@@ -8,7 +8,13 @@
 // codes. Other blocks turn the queries of the same tokens (the heads that
 // share the kv head). Bound: bytes (2 per element read, 1 written; queries 2
 // and 2); what costs beside them is a block's chain of dependent reads (lengths,
-// page number, scale), so the tokens are fetched beside that chain.
+// page number, scale), so the tokens are fetched beside that chain. Measured: a
+// 2048-token prompt of 32 and 8 heads of 128 15 us (47 MB, 3.2 TB/s), ragged
+// chunks of 3168 tokens with 32 and 32 heads of 100 in pages of 16 45 us (102
+// MB, 2.3 TB/s: 13000 blocks with work of about 6 KB, as many without), one
+// token of 16 sequences 6.6 us (latency). Keys and values in blocks apart, each
+// read twice, took 20, 78 and 6.6 us; two or four heads a block 51 and 56 us on
+// the ragged chunks where one took 51.
 //
 // Rotation: a' = a cos - b sin, b' = b cos + a sin with every product and sum
 // rounded (no contraction), so the codes do not depend on how a compiler
@@ -430,6 +436,8 @@ int launch_append(AppendParams& p, hipStream_t stream) {
                                 rope_units(p.dim, 0, W4_ROPE_INTERLEAVED, vec));
   const int64_t per_head = (int64_t)slots * (p.q_heads / p.kv_heads) *
                            rope_units(p.dim, p.rot, p.style, vec);
+  // threads by the units of a page and head. 1024 units (64 slots of 128 dims):
+  // 512 threads x 2 13.9 us on the 2048-token prompt, 256 x 4 16.0, 1024 x 1 17.7
 #define W4_AP(VEC, NT, U)                                                                       \
   do {                                                                                          \
     /* queries of as many kv heads as give each thread four units */                            \

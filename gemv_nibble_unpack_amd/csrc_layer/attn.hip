@@ -26,8 +26,16 @@
 //
 // Chunks: a sequence's chunks are joined by the block that arrives last
 // (agent-scope stores and loads, one arrival counter per row tile, left zero).
-// Bound: the bytes of the codes (2 per cached token, head and dim).
-
+//
+// Bound: the bytes of the codes (2 per cached token, head and dim). One token
+// over 131072 cached ones of 8 heads of 128 takes 56 us (4.8 TB/s; a plain read
+// of as many bytes 42), 32 sequences of 1 to 4096 tokens 34 us (4.0 TB/s, the
+// blocks of the longest last), one token over 517 cached 7.8 us (a chain of
+// dependent reads: length, page number, codes, parts). Widening in registers
+// costs about 51 codes a clock and CU, 4 times what memory delivers, so nothing
+// is staged through LDS. Keeping two steps' codes in registers at once measured
+// slower (68 us on the long one, for the registers it takes) than fetching
+// into the registers that the last step freed.
 #include "attn.hpp"
 
 namespace w4 {
@@ -442,7 +450,12 @@ inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int grou
                           int dp) {
   AttnPlan a{};
   const int64_t rows = (int64_t)max_q * group;
-  a.many = rows > 32;
+  // Rows by sequence and kv head. Up to 16 fill one operand of k_attn_few, up to
+  // 64 are two or four tiles of its 32-row form. 4 sequences of 3000 to 4000
+  // cached tokens, 8 kv heads of 128: 20 rows 21 us against k_attn_many's 31,
+  // 64 rows 24 against 31, 96 rows 27 against 33; 32 sequences of 500 to 1000: 64
+  // rows 23.5 against 26.8, 96 rows 31.6 against 28.5.
+  a.many = rows > 64;
   a.qt = rows > 16 ? 2 : 1;
   const int tile = a.many ? MANY_ROWS * (many_pair(dp) ? 2 : 1) : 16 * a.qt;
   a.tiles = (int)((rows + tile - 1) / tile);

@@ -5,7 +5,11 @@
 // 1/sqrt(S/K + eps), its scale max|y|/L = G * r / L (L = 127 or 448), and the
 // codes y / scale = g * (L / G): the root cancels, so both reductions are
 // taken together and the row is coded from the registers it was loaded into.
-// Bound: bytes (fp16 with residual: 4 read, 3 written per element).
+// Bound: bytes (fp16 with residual: 4 read, 3 written per element). 2048 rows of
+// 4096 in fp16 with residual take 11.3 us, 5.2 TB/s (a large copy reaches 4.8);
+// 333 float32 rows of 8640 take 4.9 us, 2.9 TB/s, one row of 4096 2.1 us, both
+// of them launch and latency. A row's chunks are all loaded before any is used:
+// one round trip to memory, one barrier.
 
 #include "layer_common.hpp"
 
@@ -158,6 +162,8 @@ int launch_norm(const void* X, const void* R, const void* Wt, int M, int K, floa
   hipLaunchKernelGGL((k_add_rmsnorm<T, Q, WV, C>), dim3(ceil_div(M, WV < 4 ? 4 / WV : 1)),       \
                      dim3(WV < 4 ? 256 : 64 * WV), 0, stream, (const T*)X, (const T*)R,          \
                      (const T*)Wt, M, K, eps, (T*)H, (uint8_t*)Yq, scale)
+  // waves by the row: 4096 rows of 512 4.8 us on one wave each, 6.6 on four; 2048
+  // rows of 4096 11.3 us on four, 11.7 on eight (one row 4.7 and 4.5)
   if (K <= 1024) W4_NORM(1, 2);
   else if (K <= 4096) W4_NORM(4, 2);
   else if (K <= 8192) W4_NORM(8, 2);
