@@ -30,7 +30,7 @@
 // arrives that is more than twice r, the largest one at the last such turn;
 // until then weights in units of r stay below 2^9, which P_UP_MANY = 2^6 keeps
 // inside fp16 (below 2^15).
-
+//
 // Bound: instruction issue. A wave's step is 32 matrix instructions (1024 clocks
 // of the matrix core) and about 340 vector ones beside 32 exponentials; vector
 // instructions issue only in about half of a matrix instruction's clocks, and
@@ -82,6 +82,26 @@ struct AttnMany {
   static_assert(ROWS * (OROW + 3) * 4 <= 2 * NS * STAGE, "the join fits the stages");
 };
 
+// The sequence that takes the rank-th place by cached length, longest first
+// (equal ones by number): blocks start in the order of their ids, and what
+// starts last should be short. 4, 8, 16 and 32 sequences of 20 to 900 new tokens
+// over 950 to 4800, in any order, 32 and 8 heads of 128: 154, 212, 416 and 851
+// us; in the caller's order, pairs slowest, 285, 395, 602 and 1067. Batches above
+// a wave's lanes have blocks for many rounds and keep their order. (In the
+// kernel of few rows the lookup costs more than the order gives: 64 single
+// tokens over 2 to 4096 67 to 62 us, but 32 over 1500 24.6 to 26.9.)
+__device__ __forceinline__ int by_length(const AttnParams& p, int rank) {
+  if (p.batch == 1 || p.batch > 64) return rank;
+  const int lane = threadIdx.x & 63;
+  const int mine = lane < p.batch ? p.kv_len[lane] : 0;
+  int before = 0;
+  for (int j = 0; j < p.batch; ++j) {
+    const int other = __builtin_amdgcn_readlane(mine, j);
+    before += other > mine || (other == mine && j < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < p.batch && before == rank));
+}
+
 template <int DP, int Q>
 __global__ __launch_bounds__(AttnMany<DP>::THREADS) void k_attn_many(const AttnParams p) {
   using C = AttnMany<DP>;
@@ -89,14 +109,15 @@ __global__ __launch_bounds__(AttnMany<DP>::THREADS) void k_attn_many(const AttnP
   unsigned* slast = reinterpret_cast<unsigned*>(smem + C::LDS - 16);
 
   // heads fastest (a head's blocks share an XCD's L2 when kv_heads is a
-  // multiple of 8), then splits and sequences, pairs of row tiles slowest
+  // multiple of 8), then the pairs of row tiles of a sequence, which read the same
+  // codes, then sequences from the longest, parts slowest
   int t = blockIdx.x;
   const int h = t % p.kv_heads;
   t /= p.kv_heads;
-  const int split = t % p.splits;
-  t /= p.splits;
-  const int b = t % p.batch;
-  const int pair = t / p.batch;
+  const int pair = t % p.tiles;
+  t /= p.tiles;
+  const int b = by_length(p, t % p.batch);
+  const int split = t / p.batch;
 
   int row0, n, len;
   bool fits;

@@ -605,6 +605,18 @@ def test_attention_many_rows_split(g, kind, n):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("batch", [2, 64, 65])
+def test_attention_many_sequences(g, batch):
+    """Tiled attention of batches in any order of lengths, equal lengths among them."""
+    rng = np.random.default_rng(39)
+    news = [150 if b == batch // 2 else int(rng.integers(0, 4)) for b in range(batch)]
+    lens = [max(n, int(rng.choice([0, 1, 40, 40, 200, 333]))) for n in news]
+    cache, table = random_cache(rng, lens, 16, 1, 64, 64, 0)
+    spoil_past_end(cache, table, lens)
+    _, w = check_attention(g, rng, cache, table, lens, news, 2)
+    say("sequences", batch, "worst share of the bound", round(w, 3))
+
+
 @pytest.mark.parametrize("n", [1, 4])
 def test_attention_split_repeats_bitwise_and_shares_workspace(g, n):
     """Long sequences are split over blocks: the same bits call after call, on another
