@@ -9,12 +9,13 @@
 // share the kv head). Bound: bytes (2 per element read, 1 written; queries 2
 // and 2); what costs beside them is a block's chain of dependent reads (lengths,
 // page number, scale), so the tokens are fetched beside that chain. Measured: a
-// 2048-token prompt of 32 and 8 heads of 128 15 us (47 MB, 3.2 TB/s), ragged
-// chunks of 3168 tokens with 32 and 32 heads of 100 in pages of 16 45 us (102
-// MB, 2.3 TB/s: 13000 blocks with work of about 6 KB, as many without), one
-// token of 16 sequences 6.6 us (latency). Keys and values in blocks apart, each
-// read twice, took 20, 78 and 6.6 us; two or four heads a block 51 and 56 us on
-// the ragged chunks where one took 51.
+// 2048-token prompt of 32 and 8 heads of 128 13.7 us (47 MB, 3.4 TB/s), ragged
+// chunks of 3168 tokens with 32 and 32 heads of 100 in pages of 16 39.5 us (102
+// MB, 2.6 TB/s: 8000 blocks with work of about 12 KB, as many without; half of
+// the time the vector units are busy), one token of 16 sequences 6.0 us (latency;
+// 6.9 with plain divisions of the block number). Keys and values in blocks
+// apart, each read twice, took 20, 78 and 6.6 us; two or four heads a block 51
+// and 56 us on the ragged chunks where one took 51.
 //
 // Rotation: a' = a cos - b sin, b' = b cos + a sin with every product and sum
 // rounded (no contraction), so the codes do not depend on how a compiler
@@ -38,7 +39,18 @@ struct AppendParams {
   int columns;        // pages a sequence's new tokens can touch
   int q_span;         // kv heads whose queries one block turns
   int q_blocks;       // blocks of queries per page (0 without queries)
+  uint32_t per_page_inv, columns_inv;   // floor_inv of blocks per page, of columns
 };
+
+// n / d for n below 2^32 with inv = floor(2^32 / d) (2^32 - 1 for d = 1): the high
+// word of n * inv is the quotient or one less.
+inline uint32_t floor_inv(uint32_t d) {
+  return d == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / d);
+}
+__device__ __forceinline__ uint32_t div_inv(uint32_t n, uint32_t d, uint32_t inv) {
+  const uint32_t q = __umulhi(n, inv);
+  return q + (n - q * d >= d ? 1u : 0u);
+}
 
 // The new tokens of sequence b: first row, count, first position. False if
 // there are none or the lengths do not fit (see the header).
@@ -125,11 +137,25 @@ __device__ __forceinline__ Angle<VEC> load_angle(const float* cs, int d0, int d1
     return a;
   }
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {               // pairs of y0, then pairs of y1
-    const int d = (e < VEC / 2 ? d0 : d1 >= 0 ? d1 : d0) + 2 * (e % (VEC / 2));
+  for (int v = 0; v < 2; ++v) {                 // pairs of y0, then pairs of y1
+    // a vector turns as a whole or not at all (rot is a multiple of 4)
+    const int d = v == 0 || d1 < 0 ? d0 : d1;
     const bool in = d < rot;
-    a.c[e] = in ? cs[d / 2] : 1.f;
-    a.s[e] = in ? cs[half + d / 2] : 0.f;
+    const float* t = cs + (in ? d / 2 : 0);
+    float c[VEC / 2], z[VEC / 2];
+    if (rot) {
+      if constexpr (VEC == 4) {
+        load_vec<float, 2>(t, c);
+        load_vec<float, 2>(t + half, z);
+      } else {
+        c[0] = t[0], z[0] = t[half];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      a.c[v * (VEC / 2) + e] = in ? c[e] : 1.f;
+      a.s[v * (VEC / 2) + e] = in ? z[e] : 0.f;
+    }
   }
   return a;
 }
@@ -180,6 +206,13 @@ __device__ __forceinline__ float scale_for(uint32_t m) {
 template <int Q, int VEC>
 __device__ __forceinline__ uint32_t codes_of(const float (&y)[VEC], float s) {
   if (!(s > 0.f)) return 0u;
+  if constexpr (Q == W4_Q_F8) {
+    // s is a power of two from 2^-126 to 2^120 (as this kernel makes them), its reciprocal exact: the
+    // product is the quotient bit for bit (ragged chunks 43.8 us divided, 40.9 so)
+    const float r = 1.0f / s;
+    if constexpr (VEC == 4) return code4<Q>(y[0] * r, y[1] * r, y[2] * r, y[3] * r);
+    else return code4<Q>(y[0] * r, y[1] * r, 0.f, 0.f);
+  }
   if constexpr (VEC == 4) return code4<Q>(y[0] / s, y[1] / s, y[2] / s, y[3] / s);
   else return code4<Q>(y[0] / s, y[1] / s, 0.f, 0.f);
 }
@@ -203,16 +236,15 @@ __global__ __launch_bounds__(NT) void k_rope_append(const AppendParams p, int im
   __shared__ uint32_t shm[2][NT / 64];
   // along one page: a block for each kv head, then blocks of q_span kv heads'
   // queries
-  int t = blockIdx.x;
   const int per_page = p.kv_heads + p.q_blocks;
-  const int which = t % per_page;
-  t /= per_page;
-  const int b = t / p.columns;
+  const int t = div_inv(blockIdx.x, per_page, p.per_page_inv);
+  const int which = blockIdx.x - t * per_page;
+  const int b = div_inv(t, p.columns, p.columns_inv);
   const int j = t - b * p.columns;
   int row, n, start;
   if (!append_span(p, b, row, n, start)) return;
   const int P = p.page, D = p.dim, DP = p.dp;
-  const int col = start / P + j;
+  const int col = (start >> __builtin_ctz(P)) + j;
   const int lo = max(start, col * P), hi = min(start + n, (col + 1) * P);   // new positions
   if (lo >= hi) return;
   const int cnt = hi - lo;
@@ -443,6 +475,8 @@ int launch_append(AppendParams& p, hipStream_t stream) {
     /* queries of as many kv heads as give each thread four units */                            \
     p.q_span = (int)max((int64_t)1, min((int64_t)p.kv_heads, 4 * NT / per_head));               \
     p.q_blocks = p.q ? (p.kv_heads + p.q_span - 1) / p.q_span : 0;                              \
+    p.per_page_inv = floor_inv(p.kv_heads + p.q_blocks);                                        \
+    p.columns_inv = floor_inv(p.columns);                                                       \
     const int64_t blocks = (int64_t)p.batch * p.columns * (p.kv_heads + p.q_blocks);            \
     if (blocks * NT > 0x7fffffff) return W4_ERR_SHAPE;                                          \
     hipLaunchKernelGGL((k_rope_append<T, Q, VEC, NT, U>), dim3((unsigned)blocks), dim3(NT),     \
