@@ -470,13 +470,15 @@ inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int grou
       const int64_t room = (W4_ATTN_WORKSPACE_MAX - WS_COUNTERS) / ((int64_t)tile * (dp + 4) * 4);
       // One block a CU at a time. The number of chunks with the shortest run
       // of whole rounds over the 256 CUs, a part's store and load costing as
-      // much as 65 tokens: 256 tokens of 32 heads over 16384 cached ones take
+      // much as 45 tokens: 256 tokens of 32 heads over 16384 cached ones take
       // 463 us unsplit, 99 us in 9 chunks; 2048 tokens over themselves (256
-      // blocks already) 55 us unsplit, 56 in 2.
+      // blocks already) 55 us unsplit, 56 in 2. 119 tokens of 16 heads over 9424:
+      // dims of 128, 192, 256 44.9, 62.3, 78.8 us; at 65 tokens (fewer parts)
+      // 44.0, 63.4, 80.5, at 130 with dims above 128 74 and 92.
       const int64_t most = min((int64_t)((max_kv + 511) / 512), room / slots);
       double best = 1e30;
       for (int64_t s = 1; s <= max(most, (int64_t)1) && s <= 256; ++s) {
-        const double cost = (double)((slots * s + 255) / 256) / s + (s > 1 ? 65.0 * s / max_kv : 0.0);
+        const double cost = (double)((slots * s + 255) / 256) / s + (s > 1 ? 45.0 * s / max_kv : 0.0);
         if (cost < best) best = cost, splits = s;
       }
     } else {
@@ -490,7 +492,10 @@ inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int grou
                                    (target + a.units / 2) / a.units));
     }
   }
-  a.chunk = (int)(((max_kv + splits - 1) / splits + least - 1) / least * least);
+  // whole steps of a block's four waves, whole turns of k_attn_many (in steps of
+  // 256 the case above takes 84 us where it takes 80)
+  const int unit = a.many ? 128 : least;
+  a.chunk = (int)(((max_kv + splits - 1) / splits + unit - 1) / unit * unit);
   a.splits = max(1, (max_kv + a.chunk - 1) / a.chunk);
   a.ws = a.splits == 1 ? 0
                        : WS_COUNTERS + (size_t)slots * a.splits * tile * (dp + (a.many ? 4 : 2)) * 4;
