@@ -441,7 +441,8 @@ __global__ __launch_bounds__(256, DP < 256 && DP * QT <= 256 ? 2 : 1) void k_att
 // workspace they need.
 struct AttnPlan {
   bool many;                       // k_attn_many
-  int qt, tiles, chunk, splits;
+  bool by_row;                     // parts numbered by row (part_slot)
+  int qt, tile, tiles, chunk, splits;
   int64_t units;
   size_t ws;
 };
@@ -457,7 +458,7 @@ inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int grou
   // rows 23.5 against 26.8, 96 rows 31.6 against 28.5.
   a.many = rows > 64;
   a.qt = rows > 16 ? 2 : 1;
-  const int tile = a.many ? MANY_ROWS * (many_pair(dp) ? 2 : 1) : 16 * a.qt;
+  const int tile = a.tile = a.many ? MANY_ROWS * (many_pair(dp) ? 2 : 1) : 16 * a.qt;
   a.tiles = (int)((rows + tile - 1) / tile);
   a.units = (int64_t)batch * kv_heads * a.tiles;
   constexpr int least = 256;
@@ -465,8 +466,10 @@ inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int grou
   if (a.units <= WS_COUNTER_SLOTS) {
     if (a.many) {
       // blocks with work, at most: a ragged batch has fewer than its longest
-      // sequence's tiles times its size
-      slots = min(a.units, ((int64_t)tokens * group / tile + batch) * kv_heads);
+      // sequence's tiles times its size. Parts are numbered by the smaller count.
+      const int64_t by_row = ((int64_t)tokens * group / tile + batch) * kv_heads;
+      a.by_row = by_row < a.units;
+      slots = min(a.units, by_row);
       const int64_t room = (W4_ATTN_WORKSPACE_MAX - WS_COUNTERS) / ((int64_t)tile * (dp + 4) * 4);
       // One block a CU at a time. The number of chunks with the shortest run
       // of whole rounds over the 256 CUs, a part's store and load costing as
@@ -497,8 +500,7 @@ inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int grou
   const int unit = a.many ? 128 : least;
   a.chunk = (int)(((max_kv + splits - 1) / splits + unit - 1) / unit * unit);
   a.splits = max(1, (max_kv + a.chunk - 1) / a.chunk);
-  a.ws = a.splits == 1 ? 0
-                       : WS_COUNTERS + (size_t)slots * a.splits * tile * (dp + (a.many ? 4 : 2)) * 4;
+  a.ws = a.splits == 1 ? 0 : WS_COUNTERS + (size_t)(slots * part_bytes(a.many, tile, dp, a.splits));
   return a;
 }
 
@@ -539,6 +541,33 @@ extern "C" size_t paged_attn_kv8_workspace_bytes(int batch, int tokens, int max_
                    kv8_padded_dim(head_dim)).ws;
 }
 
+// For the tests, not in the header: the slots of a call's parts (-1 without
+// a block) in slots[batch * kv_heads * tiles], q_indptr being host memory, and
+// the bytes of a slot; returns their count, 0 if the call is not split.
+extern "C" int64_t w4_attn_part_slots(int batch, int tokens, int max_q, int max_kv, int q_heads,
+                                      int kv_heads, int head_dim, const int32_t* q_indptr,
+                                      int64_t* slots, int64_t capacity, int64_t* bytes) {
+  if (paged_attn_kv8_workspace_bytes(batch, tokens, max_q, max_kv, q_heads, kv_heads, head_dim) == 0)
+    return 0;
+  const int group = q_heads / kv_heads, dp = kv8_padded_dim(head_dim);
+  max_q = min(max_q, tokens);
+  const AttnPlan a = attn_plan(batch, tokens, max_q, max_kv, group, kv_heads, dp);
+  *bytes = part_bytes(a.many, a.tile, dp, a.splits);
+  if (a.units > capacity) return a.units;
+  for (int b = 0; b < batch; ++b) {
+    const int row0 = q_indptr ? q_indptr[b] : b, end = q_indptr ? q_indptr[b + 1] : b + 1;
+    const bool live = row0 >= 0 && end > row0 && end <= tokens;
+    const int64_t rows = live ? (int64_t)min(end - row0, max_q) * group : 0;
+    for (int h = 0; h < kv_heads; ++h)
+      for (int t = 0; t < a.tiles; ++t)
+        slots[((int64_t)b * kv_heads + h) * a.tiles + t] =
+            (int64_t)t * a.tile < rows
+                ? part_slot(a.by_row, b, h, t, row0, group, a.tile, a.tiles, kv_heads)
+                : -1;
+  }
+  return a.units;
+}
+
 extern "C" int paged_attn_kv8(const uint16_t* q, int64_t q_stride, const void* k_codes,
                               const void* v_codes, const float* k_scale, const float* v_scale,
                               const int32_t* q_indptr, const int32_t* kv_len,
@@ -577,7 +606,7 @@ extern "C" int paged_attn_kv8(const uint16_t* q, int64_t q_stride, const void* k
   p.batch = batch, p.tokens = tokens, p.max_kv = max_kv, p.cols = table_cols;
   p.q_heads = q_heads, p.kv_heads = kv_heads, p.group = q_heads / kv_heads, p.dim = head_dim;
   p.page_shift = __builtin_ctz(page_size), p.pages = num_pages;
-  p.tiles = a.tiles, p.chunk = a.chunk, p.splits = a.splits;
+  p.tiles = a.tiles, p.chunk = a.chunk, p.splits = a.splits, p.by_row = a.by_row;
   if (a.many) {
     if (a.units * a.splits > 0x7fffff) return W4_ERR_SHAPE;
     return launch_attn_many(p, dp, q_dtype, a.units * a.splits, stream);

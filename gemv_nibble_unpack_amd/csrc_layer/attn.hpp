@@ -23,10 +23,32 @@ struct AttnParams {
   int page_shift, pages;
   int tiles;                // row tiles (k_attn_many: blocks' worth of them) of max_q * group rows
   int chunk, splits;        // cached tokens per block (a multiple of 64), blocks along them
+  int by_row;               // k_attn_many: how its parts are numbered (see part_slot)
 };
 
 constexpr int MANY_ROWS = 128;    // query rows of a tile of k_attn_many
 constexpr bool many_pair(int dp) { return dp <= 128; }   // two tiles a block
+
+// The place of the parts of (sequence b, kv head h, row tile or pair of tiles),
+// counted in sets of `splits` parts. Numbered by unit there are batch * tiles *
+// kv_heads of them. A ragged batch has far more tiles than work; numbered by
+// row (`by_row`), a sequence's places start where its first row falls among
+// all rows, cut into `tile` rows: it has at most ceil(n * group / tile) tiles, so
+// with row0 + n <= tokens every place is below (tokens * group / tile + batch) *
+// kv_heads, and sequences that follow each other do not meet. The plan takes
+// the smaller of the two and the kernels number as it says.
+__host__ __device__ __forceinline__ int64_t part_slot(bool by_row, int b, int h, int t, int row0,
+                                                      int group, int tile, int tiles,
+                                                      int kv_heads) {
+  return by_row ? ((int64_t)row0 * group / tile + b + t) * kv_heads + h
+                : ((int64_t)b * kv_heads + h) * tiles + t;
+}
+// workspace bytes of a set of parts: rows' outputs and the statistics (M, L), which
+// k_attn_many keeps for every lane
+constexpr int64_t part_bytes(bool many, int tile, int dp, int splits) {
+  return (int64_t)splits * tile * (dp + (many ? 4 : 2)) * 4;
+}
+
 int launch_attn_many(const AttnParams& p, int dp, int kind, int64_t blocks, hipStream_t stream);
 
 // Sequence b's query rows and cached length. False: no new tokens, or ones

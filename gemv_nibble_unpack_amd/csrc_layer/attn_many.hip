@@ -402,11 +402,9 @@ __global__ __launch_bounds__(AttnMany<DP>::THREADS) void k_attn_many(const AttnP
   };
   // A part of a split sequence is the block's registers in lane order (waves
   // 0-3 tile A, 4-7 tile B), O in absolute units, then (M, L).
-  // A sequence's parts start at a slot that its first row fixes (the pairs of
-  // the sequences before it are at most row0 * group / rows-a-block + b).
   const size_t unit = ((size_t)b * p.kv_heads + h) * p.tiles + pair;
-  const size_t slot = ((size_t)((int64_t)row0 * p.group / (C::ROWS * C::PAIR)) + b + pair) *
-                      p.kv_heads + h;
+  const size_t slot =
+      part_slot(p.by_row, b, h, pair, row0, p.group, C::ROWS * C::PAIR, p.tiles, p.kv_heads);
   constexpr size_t PART = (size_t)C::THREADS * (C::DT * 16 + 2), NEXT = 2 * C::THREADS;
   uint32_t* po = reinterpret_cast<uint32_t*>(p.part) + slot * p.splits * PART + 2 * tid;
   // what the wave has of its rows: the output, or its part

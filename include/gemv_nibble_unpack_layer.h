@@ -158,7 +158,9 @@ size_t paged_attn_kv8_workspace_bytes(int batch, int tokens, int max_q, int max_
  *   do not fit (more than max_q new tokens: its first max_q; kv_len negative,
  *   above max_kv or past table_cols * page_size) and rows that see a token on a
  *   page number outside [0, num_pages) get NaN; a sequence whose q_indptr is
- *   decreasing or outside [0, tokens] is skipped.
+ *   decreasing or outside [0, tokens] is skipped (if that lets other sequences
+ *   share rows or take them out of order, their outputs are unspecified, and
+ *   still nothing is read or written out of bounds).
  * Errors as rope_append_kv8 (W4_ERR_ARG also for a sm_scale that is not
  * finite), plus W4_ERR_WORKSPACE.
  */
