@@ -450,6 +450,7 @@ struct AttnPlan {
 inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int group, int kv_heads,
                           int dp) {
   AttnPlan a{};
+  max_kv = max(max_kv, 1);         // nothing cached: one block writes the empty rows
   const int64_t rows = (int64_t)max_q * group;
   // Rows by sequence and kv head. Up to 16 fill one operand of k_attn_few, up to
   // 64 are two or four tiles of its 32-row form. 4 sequences of 3000 to 4000

@@ -83,3 +83,23 @@ def test_rows_before_the_first_and_past_max_q_stay_inside(g, D):  # noqa: F811
     rng = np.random.default_rng(D + 1)
     check_split(g, rng, [5000], [900, 1000], 100, 4, 1, D, 64, 1)
     check_split(g, rng, [5000, 3000], [0, 400, 500], 100, 4, 1, D, 64, 0)
+
+
+@pytest.mark.parametrize("n", [1, 5, 200])
+def test_nothing_cached(g, n):  # noqa: F811
+    """max_kv = 0: every row sees nothing; a longer sequence does not fit the bound."""
+    rng = np.random.default_rng(n)
+    cache, table = random_cache(rng, [20, 20], 16, 1, 64, 64, 0)
+    cd = (device_codes(cache, 0), device_codes(cache, 1), dev(cache.scale[0]), dev(cache.scale[1]),
+          dev(table))
+    q = dev(rng.standard_normal((2 * n, 2, 64)).astype(np.float16))
+    indptr = dev(np.array([0, n, 2 * n], np.int32))
+    lse = torch.zeros(2 * n, 2, device="cuda")
+    for lens in ([0, 0], [0, 20]):
+        out = host(g.paged_attn_kv8(q, *cd, dev(np.array(lens, np.int32)), 0, q_indptr=indptr, max_q=n,
+                                    lse=lse))
+        assert not out[:n].any() and np.isneginf(host(lse)[:n]).all()
+        if lens[1]:
+            assert np.isnan(out[n:]).all() and np.isnan(host(lse)[n:]).all()
+        else:
+            assert not out[n:].any() and np.isneginf(host(lse)[n:]).all()

@@ -101,3 +101,11 @@ def test_lengths_that_contradict_the_bound_fit():
             assert check(None, max_q, 30000, 4, 1, D, indptr=[900, 1000])
             assert check(None, max_q, 30000, 4, 1, D, indptr=[0, 990, 1000])
             assert check(None, max_q, 30000, 4, 1, D, indptr=[500, 500, 400, 1000, 70], tokens=1000)
+
+
+@pytest.mark.parametrize("max_q", [1, 5, 200])
+def test_nothing_cached_needs_no_workspace(max_q):
+    """A bound of zero on the cached tokens is a size like others."""
+    for batch in (1, 3, 100):
+        for D in (64, 256):
+            assert G.paged_attn_kv8_workspace_bytes(batch, batch * max_q, max_q, 0, 8, 2, D) == 0
