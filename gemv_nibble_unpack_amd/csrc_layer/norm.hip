@@ -113,8 +113,9 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void k_add_rmsnorm(
   const float up = gm < 0x1p-64f ? 0x1p64f : 1.0f;
   const bool bad = mx >= F32_INF;
   const float inv = bad || mx == 0 ? 0.f : L / (gm * up);
+  // (products that are all zero have scale 0 also where eps = 0 makes the root infinite)
   if (live && tid == 0)
-    scale[m] = bad ? __uint_as_float(0x7FC00000u) : gm * root / L;
+    scale[m] = bad ? __uint_as_float(0x7FC00000u) : mx == 0 ? 0.f : gm * root / L;
   uint8_t* out = Yq + base;
   auto emit = [&](int c, const float (&v)[8]) {
     u2 w = {0u, 0u};
