@@ -88,34 +88,87 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void k_add_rmsnorm(
       }
     }
   }
-  ss = wave_sum_f(ss);
   mx = wave_max_u(mx);
-  if constexpr (WAVES > 1) {
-    const int wv = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
-      shs[wv] = ss;
-      shm[wv] = mx;
-    }
-    __syncthreads();
-    ss = 0.f;
-    mx = 0;
+  // the row's sum over its waves; `first` also takes the maximum across
+  auto across = [&](bool first) {
+    ss = wave_sum_f(ss);
+    if constexpr (WAVES > 1) {
+      const int wv = threadIdx.x >> 6;
+      if (!first) __syncthreads();               // shs is read out
+      if ((threadIdx.x & 63) == 0) {
+        shs[wv] = ss;
+        if (first) shm[wv] = mx;
+      }
+      __syncthreads();
+      ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < WAVES; ++i) {
-      ss += shs[sub * WAVES + i];
-      mx = max(mx, shm[sub * WAVES + i]);
+      for (int i = 0; i < WAVES; ++i) ss += shs[sub * WAVES + i];
+      if (first) {
+        mx = 0;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) mx = max(mx, shm[sub * WAVES + i]);
+      }
     }
-  }
+  };
+  across(true);
   constexpr float L = Q == W4_Q_I8 ? 127.f : 448.f;
   const float gm = __uint_as_float(mx);
-  const float root = 1.0f / sqrtf(ss / (float)K + eps);
+  const bool bad = mx >= F32_INF;
   // a row whose largest product is below 2^-64 is coded after a multiplication
   // by 2^64, so that L / G stays finite
   const float up = gm < 0x1p-64f ? 0x1p64f : 1.0f;
-  const bool bad = mx >= F32_INF;
   const float inv = bad || mx == 0 ? 0.f : L / (gm * up);
-  // (products that are all zero have scale 0 also where eps = 0 makes the root infinite)
-  if (live && tid == 0)
-    scale[m] = bad ? __uint_as_float(0x7FC00000u) : mx == 0 ? 0.f : gm * root / L;
+  // the row's scale: the codes do not need the root
+  auto settle = [&] {
+    float mean = ss / (float)K + eps;
+    // Float32 rows whose squares leave float32 (fp16 ones cannot): the squares are
+    // summed again with h taken times 2^100 or 2^-80, as the mean is small or
+    // infinite. The same for all threads of a row, and a row with barriers has
+    // its block to itself.
+    float f = 1.f;
+    if constexpr (sizeof(T) == 4) {
+      static_assert(WAVES == 1 || WAVES >= 4, "a row with barriers has its block to itself");
+      if (__builtin_expect(!(mean >= 0x1p-100f && mean < __builtin_inff()) && !bad && mx != 0, 0)) {
+        f = mean < 1.f ? 0x1p100f : 0x1p-80f;
+        ss = 0.f;
+        if constexpr (CPT > 0) {
+#pragma unroll
+          for (int i = 0; i < CPT; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float a = tid + i * LANES < nch ? h[i][e] * f : 0.f;
+              ss += a * a;
+            }
+        } else {
+          for (int c = tid; c < nch; c += LANES) {
+            float a[8], b[8];
+            load8f(x + 8 * c, a);
+            if (r) load8f(r + 8 * c, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              a[e] = (r ? a[e] + b[e] : a[e]) * f;
+              ss += a[e] * a[e];
+            }
+          }
+        }
+        across(false);
+        mean = ss / (float)K + eps * f * f;
+      }
+    }
+    const float root = 1.0f / sqrtf(mean);         // of the mean in units of f^-2
+    // gm * (root * f) / L, the factor taken where it brings the product towards 1
+    // (products that are all zero have scale 0 also where eps = 0 makes the root infinite)
+    if (live && tid == 0) {
+      const bool early = (gm < 1.f) == (f > 1.f);
+      scale[m] = bad ? __uint_as_float(0x7FC00000u)
+                     : mx == 0 ? 0.f : gm * (early ? f : 1.f) * root / L * (early ? 1.f : f);
+    }
+  };
+  // Rows that are read again settle before H replaces them. Of the others, those of
+  // several waves code first (one float32 row of 4096 2.75 us, 2.83 the other way
+  // round), those of one wave settle first (4096 rows of 512 3.87 us, 4.01).
+  constexpr bool late = CPT > 0 && WAVES > 1;
+  if constexpr (!late) settle();
   uint8_t* out = Yq + base;
   auto emit = [&](int c, const float (&v)[8]) {
     u2 w = {0u, 0u};
@@ -136,6 +189,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void k_add_rmsnorm(
         emit(c, g[i]);
       }
     }
+    if constexpr (late) settle();
   } else {
     for (int c = tid; c < nch; c += LANES) {
       float a[8], w[8];

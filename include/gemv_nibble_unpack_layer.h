@@ -65,6 +65,9 @@ extern "C" {
  * float32; y / y_scale is evaluated as (h * weight) * (127 / max|h * weight|),
  * where the root cancels, so a code can differ from the formula's by one where
  * the quotient lies within float32 rounding of a tie.
+ * Finite float32 rows of any magnitude keep a whole scale (the squares' sum is
+ * taken again with a factor where it leaves float32's range, or falls below
+ * 2^-100 beside a smaller eps).
  *   X, residual, residual_out [M,K], weight [K]: fp16 or float32 per in_dtype
  *   (W4_IN_F16, W4_IN_F32), 16-byte aligned. Yq 1 byte x [M,K], 16-byte
  *   aligned; y_scale float32 [M]. K a multiple of 8, at most W4_MAX_K; M >= 0
