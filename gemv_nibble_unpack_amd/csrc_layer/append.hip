@@ -202,19 +202,39 @@ __device__ __forceinline__ float scale_for(uint32_t m) {
   }
 }
 
-// the codes of VEC elements, packed (0 where s is 0 or NaN)
-template <int Q, int VEC>
-__device__ __forceinline__ uint32_t codes_of(const float (&y)[VEC], float s) {
+// The codes of VEC elements, packed (0 where s is 0 or NaN). E4M3: r is the exact
+// reciprocal of s, by which the product is the quotient bit for bit (ragged
+// chunks 43.8 us divided, 40.9 so); 0, only where U > 2: there is none.
+template <int Q, int U, int VEC>
+__device__ __forceinline__ uint32_t codes_of(const float (&y)[VEC], float s, float r) {
   if (!(s > 0.f)) return 0u;
-  if constexpr (Q == W4_Q_F8) {
-    // s is a power of two from 2^-126 to 2^120 (as this kernel makes them), its reciprocal exact: the
-    // product is the quotient bit for bit (ragged chunks 43.8 us divided, 40.9 so)
-    const float r = 1.0f / s;
+  if (Q == W4_Q_F8 && (U <= 2 || __builtin_expect(r != 0.f, 1))) {
     if constexpr (VEC == 4) return code4<Q>(y[0] * r, y[1] * r, y[2] * r, y[3] * r);
     else return code4<Q>(y[0] * r, y[1] * r, 0.f, 0.f);
   }
   if constexpr (VEC == 4) return code4<Q>(y[0] / s, y[1] / s, y[2] / s, y[3] / s);
   else return code4<Q>(y[0] / s, y[1] / s, 0.f, 0.f);
+}
+// The r of codes_of for a thread's E4M3 elements y. This kernel's own scales are
+// powers of two from 2^-126 to 2^120, whose reciprocals are exact; a page that
+// was filled elsewhere may have any. Threads of one or two units then divide them
+// here, and go on with r = 1 (a branch at every codes_of takes 35 us on the ragged
+// chunks, this 31); more units cannot be held twice, r = 0 lets codes_of divide
+// (pages of 128 61 us, 71 divided here).
+template <int U, typename Units>
+__device__ __forceinline__ float exact_reciprocal(Units& y, float s) {
+  const uint32_t b = __builtin_amdgcn_readfirstlane(__float_as_uint(s));   // one value in a block
+  if (__builtin_expect((b & 0x007FFFFFu) == 0 && b >= 0x00800000u && b < 0x7F000000u, 1))
+    return __uint_as_float(0x7F000000u - b);           // 2^-e for 2^e
+  if (U > 2) return 0.f;
+  if (s > 0.f) {
+#pragma unroll
+    for (int z = 0; z < U; ++z) {
+      for (float& e : y[z].y0) e /= s;
+      for (float& e : y[z].y1) e /= s;
+    }
+  }
+  return 1.f;
 }
 template <int VEC>
 __device__ __forceinline__ void put_codes(uint8_t* p, uint32_t w) {
@@ -367,6 +387,9 @@ __global__ __launch_bounds__(NT) void k_rope_append(const AppendParams p, int im
     p.vs[ph] = vs;
   }
 
+  const float kr = Q == W4_Q_F8 ? exact_reciprocal<U>(ky, ks) : 0.f;
+  const float vr = Q == W4_Q_F8 ? exact_reciprocal<U>(vy, vs) : 0.f;
+
   // ---- keys: earlier slots, the new ones, their padding, a begun page's rest -----
   const int pad = (DP - D) / 4;
   {
@@ -381,12 +404,12 @@ __global__ __launch_bounds__(NT) void k_rope_append(const AppendParams p, int im
     for (int z = 0; z < U; ++z) {
       int tok, d0, d1;
       if (kunit(z, tok, d0, d1)) {
-        put_codes<VEC>(dst + tok * DP + d0, codes_of<Q, VEC>(ky[z].y0, ks));
-        if (d1 >= 0) put_codes<VEC>(dst + tok * DP + d1, codes_of<Q, VEC>(ky[z].y1, ks));
+        put_codes<VEC>(dst + tok * DP + d0, codes_of<Q, U>(ky[z].y0, ks, kr));
+        if (d1 >= 0) put_codes<VEC>(dst + tok * DP + d1, codes_of<Q, U>(ky[z].y1, ks, kr));
       }
       if (vunit(z, tok, d0, d1)) {                  // values, staged as [dim][new token]
-        const uint32_t w0 = codes_of<Q, VEC>(vy[z].y0, vs);
-        const uint32_t w1 = codes_of<Q, VEC>(vy[z].y1, vs);
+        const uint32_t w0 = codes_of<Q, U>(vy[z].y0, vs, vr);
+        const uint32_t w1 = codes_of<Q, U>(vy[z].y1, vs, vr);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           img[(d0 + e) * img_row + tok] = (uint8_t)(w0 >> (8 * e));

@@ -5,7 +5,8 @@ import pytest
 
 import oracle as O
 from tests._helpers import say
-from tests.test_gpu_layer import check_norm, dev, g, host  # noqa: F401
+from tests.test_gpu_layer import (append_call, check_cache, check_norm, dev, device_codes, g,  # noqa: F401
+                                  host, rope_table)
 
 torch = pytest.importorskip("torch")
 
@@ -72,3 +73,43 @@ def test_norm_float32_row_at_the_largest_values(g):  # noqa: F811
             W = np.full(K, w, np.float32)
             codes, scale, _ = (host(t) for t in g.add_rmsnorm_q8(dev(x), dev(W), eps=eps))
             check_norm(codes, scale, x, W, None, eps, 0, (K, h, w, eps))
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("D,rot,style,n,page", [(64, 0, 0, 1, 16), (100, 100, 0, 5, 16), (128, 64, 1, 9, 16),
+                                                (128, 128, 0, 100, 128), (100, 100, 0, 120, 128)])
+def test_append_continues_pages_of_any_scale(g, D, rot, style, n, page, kind):  # noqa: F811
+    """Pages filled by someone else: their scales are no powers of two, some subnormal;
+    new elements that are ties of the codes in units of them, and zeros."""
+    rng = np.random.default_rng(D)
+    Hkv, B, lead = 2, 24, 5
+    dp = g.kv8_padded_dim(D)
+    cache = O.PagedCache8(B, page, Hkv, D, dp, kind)
+    for c in cache.codes:
+        c[:, :, :lead, :D] = rng.integers(0, 0x70, (B, Hkv, lead, D))
+    for s in cache.scale:
+        s[:] = np.exp(rng.uniform(-8, 3, s.shape)).astype(np.float32)
+        s[3], s[4], s[5], s[B - 2], s[B - 1] = 1e-40, 2.0 ** -127, 3e-38, 2.0 ** 127, 1.5 * 2.0 ** 126
+    table = np.arange(B, dtype=np.int32)[rng.permutation(B), None]
+    cdev = (device_codes(cache, 0), device_codes(cache, 1), dev(cache.scale[0]), dev(cache.scale[1]))
+    tab = rope_table(page, rot) if rot else None
+    if rot:
+        tab[:, :rot // 2], tab[:, rot // 2:] = 1, 0          # the turn keeps the ties
+    new = []
+    for s in cache.scale:
+        if kind == 0:
+            t = rng.integers(-100, 100, (B, n, Hkv, D)) + 0.5
+        else:
+            t = (rng.integers(8, 16, (B, n, Hkv, D)) + 0.5) * 2.0 ** rng.integers(-6, 4, (B, n, Hkv, D))
+        t[table[:, 0] >= B - 2] /= 1024                       # products that stay finite
+        x = (t * s[table[:, 0]][:, None, :, None]).astype(np.float32)
+        x[rng.random(x.shape) < 0.1] = 0
+        x[table[:, 0] == 3] = x[table[:, 0] == 4] = 0
+        new.append(x.reshape(B * n, Hkv, D))
+    append_call(g, cdev, (new[0], *new), table, [lead + n] * B, [n] * B, tab, style, np.float32, False,
+                with_q=False)
+    pos = np.tile(np.arange(lead, lead + n), B)
+    kr = O.rope_f32(new[0], tab, pos, rot, style)
+    for b in range(B):
+        cache.append((kr[b * n:(b + 1) * n], new[1][b * n:(b + 1) * n]), table[b], lead)
+    check_cache(cache, *cdev, (D, kind))
