@@ -39,8 +39,11 @@ struct AppendParams {
   int columns;        // pages a sequence's new tokens can touch
   int q_span;         // kv heads whose queries one block turns
   int q_blocks;       // blocks of queries per page (0 without queries)
-  uint32_t per_page_inv, columns_inv;   // floor_inv of blocks per page, of columns
+  uint32_t per_page_inv;   // floor_inv of blocks per page
 };
+
+// sequences of a launch, the y of its grid
+constexpr int BATCH_Y = 65535;
 
 // n / d for n below 2^32 with inv = floor(2^32 / d) (2^32 - 1 for d = 1): the high
 // word of n * inv is the quotient or one less.
@@ -257,10 +260,9 @@ __global__ __launch_bounds__(NT) void k_rope_append(const AppendParams p, int im
   // along one page: a block for each kv head, then blocks of q_span kv heads'
   // queries
   const int per_page = p.kv_heads + p.q_blocks;
-  const int t = div_inv(blockIdx.x, per_page, p.per_page_inv);
-  const int which = blockIdx.x - t * per_page;
-  const int b = div_inv(t, p.columns, p.columns_inv);
-  const int j = t - b * p.columns;
+  const int j = div_inv(blockIdx.x, per_page, p.per_page_inv);
+  const int which = blockIdx.x - j * per_page;
+  const int b = blockIdx.y;
   int row, n, start;
   if (!append_span(p, b, row, n, start)) return;
   const int P = p.page, D = p.dim, DP = p.dp;
@@ -499,10 +501,10 @@ int launch_append(AppendParams& p, hipStream_t stream) {
     p.q_span = (int)max((int64_t)1, min((int64_t)p.kv_heads, 4 * NT / per_head));               \
     p.q_blocks = p.q ? (p.kv_heads + p.q_span - 1) / p.q_span : 0;                              \
     p.per_page_inv = floor_inv(p.kv_heads + p.q_blocks);                                        \
-    p.columns_inv = floor_inv(p.columns);                                                       \
-    const int64_t blocks = (int64_t)p.batch * p.columns * (p.kv_heads + p.q_blocks);            \
+    const int64_t blocks = (int64_t)p.columns * (p.kv_heads + p.q_blocks);   /* a sequence */   \
     if (blocks * NT > 0x7fffffff) return W4_ERR_SHAPE;                                          \
-    hipLaunchKernelGGL((k_rope_append<T, Q, VEC, NT, U>), dim3((unsigned)blocks), dim3(NT),     \
+    const dim3 grid((unsigned)blocks, p.batch);                                                 \
+    hipLaunchKernelGGL((k_rope_append<T, Q, VEC, NT, U>), grid, dim3(NT),                       \
                        (size_t)p.dp * img_row + 16, stream, p, img_row);                        \
   } while (0)
   if (v4) {
@@ -571,10 +573,28 @@ extern "C" int rope_append_kv8(const void* q, const void* k, const void* v, int 
   p.batch = batch, p.tokens = tokens, p.max_q = min(max_q, tokens), p.cols = table_cols;
   p.q_heads = q_heads, p.kv_heads = kv_heads, p.dim = head_dim, p.dp = dp;
   p.page = page_size, p.pages = num_pages;
-  p.columns = (p.max_q + page_size - 2) / page_size + 1;
-  if (in_dtype == W4_IN_F16)
-    return q_dtype == W4_Q_I8 ? launch_append<uint16_t, W4_Q_I8>(p, stream)
-                              : launch_append<uint16_t, W4_Q_F8>(p, stream);
-  return q_dtype == W4_Q_I8 ? launch_append<float, W4_Q_I8>(p, stream)
-                            : launch_append<float, W4_Q_F8>(p, stream);
+  p.columns = (int)(((int64_t)p.max_q + page_size - 2) / page_size + 1);
+  const size_t e = in_dtype == W4_IN_F16 ? 2 : 4;
+  for (int64_t b0 = 0; b0 < batch; b0 += BATCH_Y) {  // one launch, save for huge batches
+    p.batch = (int)min(batch - b0, (int64_t)BATCH_Y);
+    const int st = in_dtype == W4_IN_F16
+                       ? (q_dtype == W4_Q_I8 ? launch_append<uint16_t, W4_Q_I8>(p, stream)
+                                             : launch_append<uint16_t, W4_Q_F8>(p, stream))
+                       : (q_dtype == W4_Q_I8 ? launch_append<float, W4_Q_I8>(p, stream)
+                                             : launch_append<float, W4_Q_F8>(p, stream));
+    if (st != W4_OK) return st;
+    p.kv_len += p.batch;
+    p.table += (int64_t)p.batch * p.cols;
+    if (p.indptr) {
+      p.indptr += p.batch;
+      continue;
+    }
+    auto rows = [&](const void* x, int64_t stride) {
+      return x ? (const uint8_t*)x + p.batch * stride * e : nullptr;
+    };
+    p.q = rows(p.q, q_stride), p.k = rows(p.k, k_stride), p.v = rows(p.v, v_stride);
+    if (p.q_out) p.q_out += (int64_t)p.batch * q_heads * head_dim;
+    p.tokens -= p.batch;
+  }
+  return W4_OK;
 }

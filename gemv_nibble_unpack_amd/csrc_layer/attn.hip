@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256, DP < 256 && DP * QT <= 256 ? 2 : 1) void k_att
   float* sref = sml + 4 * C::ROWS * 2;                              // [4]
   unsigned* slast = reinterpret_cast<unsigned*>(sref + 4);
 
-  int t = blockIdx.x;
+  int t = block_number();          // past the grid's end: split >= parts below
   const int h = t % p.kv_heads;
   t /= p.kv_heads;
   const int tile = t % p.tiles;
@@ -508,12 +508,12 @@ inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int grou
 template <int DP, int Q>
 int launch_attn(const AttnParams& p, const AttnPlan& a, hipStream_t stream) {
   const int64_t blocks = a.units * a.splits;
-  if (blocks > 0x7fffff) return W4_ERR_SHAPE;
+  if (blocks > MAX_BLOCKS) return W4_ERR_SHAPE;
 #define W4_AT(QT)                                                                       \
   do {                                                                                  \
     constexpr int lds = AttnFew<DP, Q, QT>::LDS;                                        \
     allow_smem((const void*)k_attn_few<DP, Q, QT>, lds);                                \
-    hipLaunchKernelGGL((k_attn_few<DP, Q, QT>), dim3((unsigned)blocks), dim3(256), lds, \
+    hipLaunchKernelGGL((k_attn_few<DP, Q, QT>), grid_of(blocks), dim3(256), lds,        \
                        stream, p);                                                      \
   } while (0)
   if (a.qt == 1) W4_AT(1);
@@ -609,7 +609,7 @@ extern "C" int paged_attn_kv8(const uint16_t* q, int64_t q_stride, const void* k
   p.page_shift = __builtin_ctz(page_size), p.pages = num_pages;
   p.tiles = a.tiles, p.chunk = a.chunk, p.splits = a.splits, p.by_row = a.by_row;
   if (a.many) {
-    if (a.units * a.splits > 0x7fffff) return W4_ERR_SHAPE;
+    if (a.units * a.splits > MAX_BLOCKS) return W4_ERR_SHAPE;
     return launch_attn_many(p, dp, q_dtype, a.units * a.splits, stream);
   }
 #define W4_DP(D)                                                  \

@@ -111,7 +111,7 @@ __global__ __launch_bounds__(AttnMany<DP>::THREADS) void k_attn_many(const AttnP
   // heads fastest (a head's blocks share an XCD's L2 when kv_heads is a
   // multiple of 8), then the pairs of row tiles of a sequence, which read the same
   // codes, then sequences from the longest, parts slowest
-  int t = blockIdx.x;
+  int t = block_number();          // past the grid's end: split >= parts below
   const int h = t % p.kv_heads;
   t /= p.kv_heads;
   const int pair = t % p.tiles;
@@ -569,7 +569,7 @@ template <int DP, int Q>
 static int launch(const AttnParams& p, int64_t blocks, hipStream_t stream) {
   constexpr int lds = AttnMany<DP>::LDS;
   allow_smem((const void*)k_attn_many<DP, Q>, lds);
-  hipLaunchKernelGGL((k_attn_many<DP, Q>), dim3((unsigned)blocks), dim3(AttnMany<DP>::THREADS),
+  hipLaunchKernelGGL((k_attn_many<DP, Q>), grid_of(blocks), dim3(AttnMany<DP>::THREADS),
                      lds, stream, p);
   return launch_status();
 }

@@ -116,6 +116,17 @@ __device__ __forceinline__ f4 decode4(uint32_t w) {
   }
 }
 
+// Grids of more blocks than one dimension launches (fewer than 2^32 threads along
+// x): rows of GRID_X blocks. The last row may have blocks past the end, which
+// the kernels must leave without work.
+constexpr int GRID_X = 1 << 21;
+constexpr int64_t MAX_BLOCKS = 0x7fffffff;
+inline dim3 grid_of(int64_t blocks) {
+  if (blocks <= GRID_X) return dim3((unsigned)blocks);
+  return dim3(GRID_X, (unsigned)((blocks + GRID_X - 1) / GRID_X));
+}
+__device__ __forceinline__ int block_number() { return blockIdx.y * GRID_X + blockIdx.x; }
+
 inline bool kv8_page_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
 
 }  // namespace w4

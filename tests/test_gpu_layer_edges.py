@@ -5,7 +5,7 @@ import pytest
 
 import oracle as O
 from tests._helpers import say
-from tests.test_gpu_layer import (append_call, check_cache, check_norm, dev, device_codes, g,  # noqa: F401
+from tests.test_gpu_layer import (append_call, attn_bound, check_cache, check_norm, dev, device_codes, g,  # noqa: F401
                                   host, rope_table)
 
 torch = pytest.importorskip("torch")
@@ -113,3 +113,96 @@ def test_append_continues_pages_of_any_scale(g, D, rot, style, n, page, kind):  
     for b in range(B):
         cache.append((kr[b * n:(b + 1) * n], new[1][b * n:(b + 1) * n]), table[b], lead)
     check_cache(cache, *cdev, (D, kind))
+
+
+def long_and_singles(batch, n, page):
+    """One sequence of n new tokens at the front of a batch of single ones: lengths,
+    q_indptr, page table and pool."""
+    news = np.array([n] + [1] * (batch - 1))
+    lens = news + np.arange(batch) % page
+    need = -(-lens // page)
+    table = np.full((batch, need.max()), -1, np.int32)
+    first = np.concatenate([[0], np.cumsum(need)])
+    for b in range(batch):
+        table[b, :need[b]] = first[b] + np.arange(need[b])
+    return lens.astype(np.int32), np.concatenate([[0], np.cumsum(news)]).astype(np.int32), table, int(first[-1])
+
+
+def test_append_of_a_long_prompt_in_a_large_batch(g):  # noqa: F811
+    """More blocks than one grid dimension launches: the same as the long sequence and
+    the others in calls of their own."""
+    batch, n, page, H, D = 1024, 16384, 16, 8, 64
+    lens, indptr, table, pool = long_and_singles(batch, n, page)
+    T = int(indptr[-1])
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn(T, H, D, device="cuda", generator=gen).half() for _ in range(3))
+    rope = dev(rope_table(n + page, D))
+    out = []
+    for calls in ([(0, batch, n)], [(0, 1, n), (1, batch, 1)]):
+        c = g.kv8_alloc(pool, page, H, D)
+        qo = []
+        for a, z, most in calls:
+            rows = slice(int(indptr[a]), int(indptr[z]))
+            say("append", a, z, "rows", rows)
+            qo.append(g.rope_append_kv8(q[rows], k[rows], v[rows], *c, dev(table[a:z]), dev(lens[a:z]),
+                                        q_indptr=dev(indptr[a:z + 1] - indptr[a]), max_q=most, rope=rope))
+        out.append((*c, torch.cat(qo)))
+    torch.cuda.synchronize()
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    assert all(bool(t.any()) for t in out[0])
+
+
+def test_attention_of_a_long_prompt_in_a_large_batch(g):  # noqa: F811
+    """The same for attention: sampled rows against the oracle."""
+    batch, n, page, H, D = 4096, 12400, 64, 32, 4
+    lens, indptr, table, pool = long_and_singles(batch, n, page)
+    T = int(indptr[-1])
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    c = (torch.randint(-127, 128, (pool, H, page, 64), device="cuda", generator=gen).to(torch.int8),
+         torch.randint(-127, 128, (pool, H, 64, page), device="cuda", generator=gen).to(torch.int8),
+         *(torch.rand(pool, H, device="cuda", generator=gen) / 40 for _ in range(2)))
+    c[0][..., D:] = 0
+    c[1][:, :, D:] = 0
+    q = torch.randn(T, H, D, device="cuda", generator=gen).half()
+    say("attention", batch, T)
+    out = host(g.paged_attn_kv8(q, *c, dev(table), dev(lens), int(lens.max()), q_indptr=dev(indptr),
+                                max_q=T)).astype(np.float64)
+    assert np.isfinite(out).all()
+    qh = host(q)
+    for b, i in [(0, 0), (0, 255), (0, 6001), (0, n - 1), (1, 0), (77, 0), (batch - 1, 0)]:
+        ids = torch.from_numpy(table[b, :-(-int(lens[b]) // page)].astype(np.int64)).cuda()
+        for h in (0, 31):
+            k = host(c[0][ids, h, :, :D].double() * c[2][ids, h].double()[:, None, None]).reshape(-1, D)
+            v = host((c[1][ids, h, :D].double() * c[3][ids, h].double()[:, None, None]).transpose(1, 2)
+                     .contiguous()).reshape(-1, D)
+            row, new = int(indptr[b]) + i, int(indptr[b + 1] - indptr[b])
+            ref, _, absv, terms = O.attention_rows(qh[row:row + 1, h], k, v, [int(lens[b]) - new + i + 1],
+                                                   D ** -0.5)
+            assert np.all(np.abs(out[row:row + 1, h] - ref) <= attn_bound(ref, absv, terms, int(lens[b]), D)), \
+                (b, i, h)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_append_of_more_sequences_than_a_grid_has_rows(g, given):  # noqa: F811
+    """70000 single tokens, with and without q_indptr: the same as in two calls."""
+    batch, half, H, D, page = 70000, 35000, 1, 64, 16
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(batch, H, D, device="cuda", generator=gen).half() for _ in range(3))
+    lens = dev((1 + np.arange(batch) % page).astype(np.int32))
+    table = dev(np.arange(batch, dtype=np.int32)[:, None])
+    rope = dev(rope_table(page, D))
+    out = []
+    for calls in ([(0, batch)], [(0, half), (half, batch)]):
+        c = g.kv8_alloc(batch, page, H, D)
+        qo = []
+        for a, z in calls:
+            ip = dev(np.arange(z - a + 1, dtype=np.int32)) if given else None
+            say("append", a, z, given)
+            qo.append(g.rope_append_kv8(q[a:z], k[a:z], v[a:z], *c, table[a:z], lens[a:z], q_indptr=ip,
+                                        rope=rope))
+        out.append((*c, torch.cat(qo)))
+    torch.cuda.synchronize()
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    assert bool((out[0][2] > 0).all())
