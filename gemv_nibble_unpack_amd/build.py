@@ -64,7 +64,12 @@ def _run(cmd, verbose):
 def build(verbose=True, jobs=None):
     """Compile every HIP source (in parallel, one object each) and link the
     package's shared library. Each translation unit carries its own device
-    code; no device function is called across units."""
+    code; no device function is called across units.
+
+    The Python marshalling of the decoder-layer operators is built beside it
+    where torch, Python's headers and a host C++ compiler are there; the library
+    needs none of them and is in its place before an error of the marshalling is
+    raised."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
     srcs = ([os.path.join(CSRC, s) for s in SOURCES] +
@@ -72,18 +77,24 @@ def build(verbose=True, jobs=None):
     objs = [os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(s))[0] + ".o") for s in srcs]
     cflags = [f for f in FLAGS if f != "-shared"]
     cmds = [[hipcc(), *cflags, *inc, "-c", s, "-o", o] for s, o in zip(srcs, objs)]
-    bind_obj = os.path.join(OBJ_DIR, "bind.o")
-    cmds.append(bind_compile(bind_obj))
-    jobs = jobs or min(len(cmds), max(1, (os.cpu_count() or 1)))
+    missing = bind_missing()
+    jobs = jobs or min(len(cmds) + 1, max(1, (os.cpu_count() or 1)))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
-        for f in [ex.submit(_run, c, verbose) for c in cmds]:
+        units = [ex.submit(_run, c, verbose) for c in cmds]
+        bind = None if missing else ex.submit(_build_bind_object, verbose)
+        for f in units:
             f.result()
-    tmp = OUT + ".tmp"
-    _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
-    undefined_kernels(tmp)
-    os.replace(tmp, OUT)
-    _run(bind_link(bind_obj, BIND_OUT + ".tmp"), verbose)
-    os.replace(BIND_OUT + ".tmp", BIND_OUT)
+        tmp = OUT + ".tmp"
+        _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
+        undefined_kernels(tmp)
+        os.replace(tmp, OUT)
+        if os.path.exists(BIND_OUT):
+            os.remove(BIND_OUT)        # never one of another library
+        if missing:
+            print(f"{os.path.basename(BIND_OUT)} not built: {missing}", file=sys.stderr)
+            return OUT
+        _run(bind_link(bind.result(), BIND_OUT + ".tmp"), verbose)
+        os.replace(BIND_OUT + ".tmp", BIND_OUT)
     return OUT
 
 
@@ -91,19 +102,47 @@ def _cxx():
     for c in (os.environ.get("CXX"), shutil.which("g++"), shutil.which("c++")):
         if c and shutil.which(c):
             return c
-    raise RuntimeError("no host C++ compiler found")
+    return None
 
 
 def _torch_dir():
     spec = importlib.util.find_spec("torch")          # its place, without importing it
-    return os.path.dirname(spec.origin)
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
-def bind_compile(obj):
+def bind_missing():
+    """What the marshalling module cannot be built for, or None."""
+    if _torch_dir() is None:
+        return "torch is not installed"
+    if not os.path.exists(os.path.join(_torch_dir(), "include", "c10", "hip", "HIPStream.h")):
+        return "torch is no ROCm build with headers"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h is not installed"
+    if _cxx() is None:
+        return "no host C++ compiler found"
+    return None
+
+
+def _torch_abi():
+    """torch's _GLIBCXX_USE_CXX11_ABI, asked of it in a process of its own."""
+    r = subprocess.run([sys.executable, "-c", "import torch; print(int(torch.compiled_with_cxx11_abi()))"],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"torch cannot be imported:\n{r.stderr}")
+    return int(r.stdout.split()[-1])
+
+
+def _build_bind_object(verbose):
+    obj = os.path.join(OBJ_DIR, "bind.o")
+    _run(bind_compile(obj, _torch_abi()), verbose)
+    return obj
+
+
+def bind_compile(obj, abi):
     """The command that compiles the marshalling module (host code only)."""
     inc = os.path.join(_torch_dir(), "include")
     return [_cxx(), "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
-            "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", os.path.join(ROOT, "include"), "-isystem", inc,
+            f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", os.path.join(ROOT, "include"), "-isystem", inc,
             "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
             os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"), "-I",
             sysconfig.get_paths()["include"], "-c", BIND_SOURCE, "-o", obj]
