@@ -38,9 +38,10 @@ def add_rmsnorm_q8(x, weight, residual=None, eps=1e-5, q_dtype=L.W4_Q_I8, residu
         raw = stream.cuda_stream
         if residual is not None and residual_out is None:
             residual_out = _empty(x.shape, x.dtype, _dev(x), stream)
-        if out is None:
+        if codes is None:
             codes = _empty(x.shape, torch.int8 if q_dtype == L.W4_Q_I8 else torch.uint8, _dev(x),
                            stream)
+        if scales is None:
             scales = _empty(x.shape[0], torch.float32, _dev(x), stream)
     r = (_BIND or _bind()).add_rmsnorm_q8(x, weight, residual, eps, q_dtype, residual_out, codes,
                                           scales, raw)

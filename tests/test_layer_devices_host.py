@@ -50,3 +50,28 @@ def test_attention(where):
     refuses(lambda: G.paged_attn_kv8(t["q"], t["kc"], t["vc"], t["ks"], t["vs"], t["table"], t["len"], 32,
                                      q_indptr=t["indptr"], max_q=3, lse=t["lse"], workspace=t["ws"],
                                      out=t["out"]))
+
+
+@pytest.mark.parametrize("given", ["codes", "scale", "both", "none"])
+def test_norm_outputs_left_out_come_from_the_pool_of_the_call_s_stream(given, monkeypatch):
+    from gemv_nibble_unpack_amd import layer
+    t = mixed(NORM, None, NORM)
+    stream = type("Stream", (), {"cuda_stream": 5})()
+    seen = {}
+
+    class Bind:
+        @staticmethod
+        def add_rmsnorm_q8(x, w, r, eps, kind, ro, codes, scales, raw):
+            seen.update(codes=codes, scales=scales, ro=ro, raw=raw)
+            return codes, scales, ro
+    monkeypatch.setattr(layer, "_BIND", Bind)
+    monkeypatch.setattr(layer, "_empty", lambda shape, dtype, dev, s: ("made", tuple(shape) if shape != 2 else 2,
+                                                                       dtype, s))
+    out = {"codes": (t["codes"], None), "scale": (None, t["scale"]), "both": (t["codes"], t["scale"]),
+           "none": None}[given]
+    layer.add_rmsnorm_q8(t["x"], t["w"], t["r"], out=out, stream=stream)
+    assert seen["raw"] == 5 and seen["ro"] == ("made", (2, 64), F16, stream)
+    assert seen["codes"] is t["codes"] if given in ("codes", "both") else seen["codes"] == \
+        ("made", (2, 64), I8, stream)
+    assert seen["scales"] is t["scale"] if given in ("scale", "both") else seen["scales"] == \
+        ("made", 2, F32, stream)
