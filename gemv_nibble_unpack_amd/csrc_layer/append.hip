@@ -9,11 +9,12 @@
 // share the kv head). Bound: bytes (2 per element read, 1 written; queries 2
 // and 2); what costs beside them is a block's chain of dependent reads (lengths,
 // page number, scale), so the tokens are fetched beside that chain. Measured: a
-// 2048-token prompt of 32 and 8 heads of 128 13.7 us (47 MB, 3.4 TB/s), ragged
-// chunks of 3168 tokens with 32 and 32 heads of 100 in pages of 16 39.5 us (102
+// 2048-token prompt of 32 and 8 heads of 128 14.0 us (47 MB, 3.4 TB/s), ragged
+// chunks of 3168 tokens with 32 and 32 heads of 100 in pages of 16 39.2 us (102
 // MB, 2.6 TB/s: 8000 blocks with work of about 12 KB, as many without; half of
-// the time the vector units are busy), one token of 16 sequences 6.0 us (latency;
-// 6.9 with plain divisions of the block number). Keys and values in blocks
+// the time the vector units are busy; 32.6 us repeated on the same tensors), one
+// token of 16 sequences 5.4 us (latency; 6.9 with plain divisions of the block
+// number). Keys and values in blocks
 // apart, each read twice, took 20, 78 and 6.6 us; two or four heads a block 51
 // and 56 us on the ragged chunks where one took 51.
 //
@@ -221,9 +222,9 @@ __device__ __forceinline__ uint32_t codes_of(const float (&y)[VEC], float s, flo
 // The r of codes_of for a thread's E4M3 elements y. This kernel's own scales are
 // powers of two from 2^-126 to 2^120, whose reciprocals are exact; a page that
 // was filled elsewhere may have any. Threads of one or two units then divide them
-// here, and go on with r = 1 (a branch at every codes_of takes 35 us on the ragged
-// chunks, this 31); more units cannot be held twice, r = 0 lets codes_of divide
-// (pages of 128 61 us, 71 divided here).
+// here, and go on with r = 1 (a branch at every codes_of: the ragged chunks, replayed,
+// 35 us, this 31); more units cannot be held twice, r = 0 lets codes_of divide
+// (the same chunks in pages of 128 61 us, 71 divided here).
 template <int U, typename Units>
 __device__ __forceinline__ float exact_reciprocal(Units& y, float s) {
   const uint32_t b = __builtin_amdgcn_readfirstlane(__float_as_uint(s));   // one value in a block
@@ -494,7 +495,10 @@ int launch_append(AppendParams& p, hipStream_t stream) {
   const int64_t per_head = (int64_t)slots * (p.q_heads / p.kv_heads) *
                            rope_units(p.dim, p.rot, p.style, vec);
   // threads by the units of a page and head. 1024 units (64 slots of 128 dims):
-  // 512 threads x 2 13.9 us on the 2048-token prompt, 256 x 4 16.0, 1024 x 1 17.7
+  // 512 threads x 2 13.9 us on the 2048-token prompt, 256 x 4 16.0, 1024 x 1 17.7.
+  // The 1024-thread forms (pages of 128, or of 64 with dims above 128) have 128 registers a
+  // thread: fp16 in vectors of four fits, fp16 in pairs spills 25, float32 16
+  // to 18, in pairs 53 to 58.
 #define W4_AP(VEC, NT, U)                                                                       \
   do {                                                                                          \
     /* queries of as many kv heads as give each thread four units */                            \

@@ -63,7 +63,7 @@ struct KVRegs {
   uint32_t bad;
 };
 
-// two blocks a CU where their registers allow it
+// two blocks a CU where their registers allow it (<256, INT8, 2> spills 3)
 template <int DP, int Q, int QT>
 __global__ __launch_bounds__(256, DP < 256 && DP * QT <= 256 ? 2 : 1) void k_attn_few(const AttnParams p) {
   using C = AttnFew<DP, Q, QT>;
@@ -490,7 +490,8 @@ inline AttnPlan attn_plan(int batch, int tokens, int max_q, int max_kv, int grou
       // over 131072 cached ones takes 56 us in 64 chunks, 60 in 96, 63 in
       // 128. A batch's lengths are mostly below their bound and leave blocks
       // without work: 32 sequences of 1 to 4096 tokens take 34 us in 3 chunks,
-      // 38 in 2. Chunks of 256 tokens (one step a wave) or more.
+      // 38 in 2 (the one batch that the 640 rests on). Chunks of 256 tokens (one
+      // step a wave) or more.
       const int64_t target = batch > 1 ? 640 : 512;
       splits = max((int64_t)1, min((int64_t)(max_kv + least - 1) / least,
                                    (target + a.units / 2) / a.units));

@@ -31,13 +31,17 @@
 // until then weights in units of r stay below 2^9, which P_UP_MANY = 2^6 keeps
 // inside fp16 (below 2^15).
 //
-// Bound: instruction issue. A wave's step is 32 matrix instructions (1024 clocks
-// of the matrix core) and about 340 vector ones beside 32 exponentials; vector
-// instructions issue only in about half of a matrix instruction's clocks, and
-// a turn adds the widening. A 2048-token prompt (32 heads of 128) takes 52 to 61
-// us over boxes, 560 to 660 TFLOP/s (a large fp16 library product: 1165), the
-// matrix cores busy 24% of the time; 256 rows over 8192 tokens of 256 heads 310
-// us, 890 TFLOP/s. Measured beside it: one tile of 128 rows a block, two blocks a
+// Bound: in the long run instruction issue. A wave's step is 32 matrix instructions
+// (1024 clocks of the matrix core) and about 340 vector ones beside 32 exponentials;
+// vector instructions issue only in about half of a matrix instruction's clocks,
+// and a turn adds the widening. 2048 tokens of 32 heads of 128 take 64 us for every
+// 2048 cached tokens before them (measured to 8192; 4.0 us a turn, 1.07 PFLOP/s, where a
+// large fp16 library product reaches 1165 TFLOP/s). Over themselves they take 52
+// to 61 us over boxes, 560 to 660 TFLOP/s, the matrix cores busy 24% of the time,
+// where that rate would take 32: the rest, not measured apart, are a block's start
+// and end, the masked part of the diagonal, and the second phase, whose turns fetch
+// and widen as much for half the products. 256 rows over 8192 tokens of 256 heads
+// 310 us, 890 TFLOP/s. Measured beside it: one tile of 128 rows a block, two blocks a
 // CU 74 us; both tiles in a block, but the long one's waves alone at the end 65;
 // the next step's first product under this step's exponentials 65 to 83
 // (registers).
@@ -51,7 +55,7 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 constexpr float P_UP_MANY = 64.0f, LOG2_P_UP_MANY = 6.0f;
 constexpr float M_SLACK = 8.0f, R_SLACK = 2.0f;
 constexpr float REF_MIN_MANY = 0x1p-100f;
-constexpr float RATIO_MIN = 0x1p-40f;     // smaller value scales count as this times r
+constexpr float RATIO_MIN = 0x1p-40f;     // of r; weights times this round to zero
 
 // max over the two halves of a wave, left in every lane
 __device__ __forceinline__ float halves_max(float v) {

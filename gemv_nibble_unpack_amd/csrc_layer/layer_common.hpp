@@ -117,7 +117,7 @@ __device__ __forceinline__ f4 decode4(uint32_t w) {
 }
 
 // Grids of more blocks than one dimension launches (fewer than 2^32 threads along
-// x): rows of GRID_X blocks. The last row may have blocks past the end, which
+// x): rows of GRID_X blocks, read with block_number(). The last row may have blocks past the end, which
 // the kernels must leave without work.
 constexpr int GRID_X = 1 << 21;
 constexpr int64_t MAX_BLOCKS = 0x7fffffff;

@@ -6,8 +6,8 @@
 // codes y / scale = g * (L / G): the root cancels, so both reductions are
 // taken together and the row is coded from the registers it was loaded into.
 // Bound: bytes (fp16 with residual: 4 read, 3 written per element). 2048 rows of
-// 4096 in fp16 with residual take 11.3 us, 5.2 TB/s (a large copy reaches 4.8);
-// 333 float32 rows of 8640 take 4.9 us, 2.9 TB/s, one row of 4096 2.1 us, both
+// 4096 in fp16 with residual take 11.0 us, 5.3 TB/s (a large copy reaches 4.8);
+// 333 float32 rows of 8640 take 5.0 us, 2.9 TB/s, one row of 4096 2.1 us, both
 // of them launch and latency. A row's chunks are all loaded before any is used:
 // one round trip to memory, one barrier.
 
@@ -17,8 +17,8 @@ namespace w4 {
 
 // One row per group of WAVES waves; CPT > 0: CPT chunks of 8 elements per lane
 // held in registers (K <= 512 * WAVES * CPT), loads of every chunk issued
-// before any is used. CPT == 0: rows too long for that are read three times
-// (the later reads come from L2), the residual sum being written by the last.
+// before any is used. CPT == 0: rows too long for that are read twice (the
+// second time from L2), the residual sum being written then.
 // A block of 256 threads holds 4 / WAVES rows; longer rows take one block.
 template <typename T, int Q, int WAVES, int CPT>
 __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void k_add_rmsnorm(
@@ -165,8 +165,8 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void k_add_rmsnorm(
     }
   };
   // Rows that are read again settle before H replaces them. Of the others, those of
-  // several waves code first (one float32 row of 4096 2.75 us, 2.83 the other way
-  // round), those of one wave settle first (4096 rows of 512 3.87 us, 4.01).
+  // several waves code first (one float32 row of 4096, replayed, 2.75 us, 2.83 the
+  // other way round), those of one wave settle first (4096 rows of 512 3.87 us, 4.01).
   constexpr bool late = CPT > 0 && WAVES > 1;
   if constexpr (!late) settle();
   uint8_t* out = Yq + base;
@@ -222,7 +222,9 @@ int launch_norm(const void* X, const void* R, const void* Wt, int M, int K, floa
   if (K <= 1024) W4_NORM(1, 2);
   else if (K <= 4096) W4_NORM(4, 2);
   else if (K <= 8192) W4_NORM(8, 2);
-  else if (K <= 12288) W4_NORM(8, 3);      // 333 float32 rows of 8640: 4.9 us; 16 waves x 2 6.0, 4 x 5 5.3
+  // (one shape measured, in the first form of these kernels: 333 float32 rows of 8640 4.9
+  // us, 16 waves x 2 6.0, 4 x 5 5.3)
+  else if (K <= 12288) W4_NORM(8, 3);
   else if (K <= 16384) W4_NORM(16, 2);
   else W4_NORM(16, 0);
 #undef W4_NORM

@@ -65,9 +65,10 @@ extern "C" {
  * float32; y / y_scale is evaluated as (h * weight) * (127 / max|h * weight|),
  * where the root cancels, so a code can differ from the formula's by one where
  * the quotient lies within float32 rounding of a tie.
- * Finite float32 rows of any magnitude keep a whole scale (the squares' sum is
- * taken again with a factor where it leaves float32's range, or falls below
- * 2^-100 beside a smaller eps).
+ * Float32 rows of any magnitude keep a whole scale (the squares' sum is taken
+ * again with a factor where it leaves float32's range, or falls below 2^-100
+ * beside a smaller eps); the products h * weight have float32's range: one that
+ * overflows counts as an infinity.
  *   X, residual, residual_out [M,K], weight [K]: fp16 or float32 per in_dtype
  *   (W4_IN_F16, W4_IN_F32), 16-byte aligned. Yq 1 byte x [M,K], 16-byte
  *   aligned; y_scale float32 [M]. K a multiple of 8, at most W4_MAX_K; M >= 0
@@ -150,7 +151,11 @@ size_t paged_attn_kv8_workspace_bytes(int batch, int tokens, int max_q, int max_
  *   log; NULL to skip).
  * Scores, softmax statistics and sums are float32; the codes enter the matrix
  * cores as exact fp16 values, the weights w are rounded to fp16 for the second
- * product (their relative error 2^-11, below that of the fp16 output). A token
+ * product (their relative error 2^-11, as the fp16 output's). They are rounded
+ * together with the value scales, in units of the largest one, r, that the row's
+ * block has met: where w_j * v_scale_j is below 2^-20 of the largest w times r,
+ * the error is up to 2^-31 of that product instead (the values of pages whose
+ * scales lie that far apart). A token
  * that sees nothing (kv_len too small) gets out 0 and lse -inf. Codes past a
  * sequence's length are never used, whatever they hold.
  *   q fp16 [tokens, q_heads, head_dim], tokens q_stride elements apart, heads
