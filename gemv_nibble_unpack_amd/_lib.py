@@ -25,6 +25,10 @@ W4_Q_I8, W4_Q_F8 = 0, 1
 W4_ROPE_HALF, W4_ROPE_INTERLEAVED = 0, 1
 W4_MAX_HEAD_DIM = 256
 W4_ATTN_WORKSPACE_MAX = 64 * 1024 * 1024
+# mirror include/gemv_nibble_unpack_mx.h
+W4_MX_A16, W4_MX_A8, W4_MX_A4 = 0, 1, 2
+W4_ACT_SILU, W4_ACT_GELU, W4_ACT_RELU2 = 0, 1, 2
+W4_MOE_MAX_TOKENS, W4_MOE_MAX_EXPERTS, W4_MOE_MAX_TOP = 64, 512, 16
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
@@ -81,6 +85,21 @@ LAYER_SIGNATURES = {
                             _i, _i, _i, _f, _p, _p, _p, _sz, _p]),
 }
 
+# the MXFP4 operators; the order follows their header
+MX_SIGNATURES = {
+    "quantize_mx4": (_i, [_p, _i, _i, _i, _p, _p, _p]),
+    "dequantize_mx4": (_i, [_p, _p, _i, _i, _i, _p, _p]),
+    "prepack_mx4_bytes": (_sz, [_i, _i]),
+    "prepack_mx4": (_i, [_p, _p, _i, _i, _p, _p]),
+    "unprepack_mx4": (_i, [_p, _i, _i, _p, _p, _p]),
+    "mx4_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "mx4a16_gemm": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _p, _sz, _p]),
+    "mx4a8_gemm": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _sz, _p]),
+    "mx4a4_gemm": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _sz, _p]),
+    "moe_mx4_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_mx4": (_i, [_p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
+}
+
 _LIB = None
 
 
@@ -98,7 +117,7 @@ def load():
             f"{LIB_PATH} not found: build it first (python -c 'import __graft_entry__ as g; g.build()')"
             " -- this package has no CPU fallback")
     lib = ctypes.CDLL(LIB_PATH)
-    for name, (res, args) in {**SIGNATURES, **LAYER_SIGNATURES}.items():
+    for name, (res, args) in {**SIGNATURES, **LAYER_SIGNATURES, **MX_SIGNATURES}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -21,8 +21,11 @@ SOURCES = ["quant.hip", "prepack.hip", "matmul.hip", "gemm_launch.hip", "probe.h
 # kernels carry a hash over csrc, which these sources do not change
 LAYER_CSRC = os.path.join(HERE, "csrc_layer")
 LAYER_SOURCES = ["norm.hip", "append.hip", "attn.hip", "attn_many.hip"]
+# the MXFP4 operators
+MX_CSRC = os.path.join(HERE, "csrc_mx")
+MX_SOURCES = ["mx_quant.hip", "mx_rows.hip", "mx_gemm.hip", "moe.hip"]
 OUT = os.path.join(HERE, "libgemv_nibble_unpack.so")
-# the Python marshalling of the decoder-layer operators: host code, built
+# the Python marshalling of the decoder-layer and MXFP4 operators: host code, built
 # against torch's headers, linked to OUT beside it
 BIND_SOURCE = os.path.join(LAYER_CSRC, "bind.cpp")
 BIND_OUT = os.path.join(HERE, "_layer_bind.so")
@@ -73,7 +76,8 @@ def build(verbose=True, jobs=None):
     os.makedirs(OBJ_DIR, exist_ok=True)
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
     srcs = ([os.path.join(CSRC, s) for s in SOURCES] +
-            [os.path.join(LAYER_CSRC, s) for s in LAYER_SOURCES])
+            [os.path.join(LAYER_CSRC, s) for s in LAYER_SOURCES] +
+            [os.path.join(MX_CSRC, s) for s in MX_SOURCES])
     objs = [os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(s))[0] + ".o") for s in srcs]
     cflags = [f for f in FLAGS if f != "-shared"]
     cmds = [[hipcc(), *cflags, *inc, "-c", s, "-o", o] for s, o in zip(srcs, objs)]

@@ -1,6 +1,7 @@
-// Python marshalling of the decoder-layer operators: checks torch tensors,
-// allocates outputs that the caller left out, and calls the C entry points of
-// include/gemv_nibble_unpack_layer.h. No arithmetic happens here.
+// Python marshalling of the decoder-layer and MXFP4 operators: checks torch
+// tensors, allocates outputs that the caller left out, and calls the C entry
+// points of include/gemv_nibble_unpack_layer.h and gemv_nibble_unpack_mx.h (the
+// latter in ../csrc_mx/bind_mx.hpp). No arithmetic happens here.
 //
 // These calls carry up to ten tensors each and their kernels take a few
 // microseconds for a single token, so the marshalling decides what a decode
@@ -21,6 +22,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "gemv_nibble_unpack_layer.h"
+#include "gemv_nibble_unpack_mx.h"
 
 namespace {
 
@@ -329,7 +331,13 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+#include "../csrc_mx/bind_mx.hpp"
+
 PyMethodDef methods[] = {
+    {"quantize_mx4", (PyCFunction)(void (*)())mx_quantize, METH_FASTCALL, nullptr},
+    {"dequantize_mx4", (PyCFunction)(void (*)())mx_dequantize, METH_FASTCALL, nullptr},
+    {"mx4_gemm", (PyCFunction)(void (*)())mx_product, METH_FASTCALL, nullptr},
+    {"moe_mx4", (PyCFunction)(void (*)())mx_moe, METH_FASTCALL, nullptr},
     {"add_rmsnorm_q8", (PyCFunction)(void (*)())norm, METH_FASTCALL, nullptr},
     {"rope_append_kv8", (PyCFunction)(void (*)())append, METH_FASTCALL, nullptr},
     {"paged_attn_kv8", (PyCFunction)(void (*)())attn, METH_FASTCALL, nullptr},

@@ -1,0 +1,51 @@
+// Products with MXFP4 weights: parameters and the pieces that the kernels share.
+#pragma once
+
+#include "mx_common.hpp"
+
+namespace w4 {
+
+struct MxParams {
+  const uint8_t* A;          // rows: fp16, E4M3 or E2M1 codes
+  const float* a_scale;      // A8: one a row
+  const uint8_t* a_scales;   // A4: one a block
+  const uint8_t* Wp;
+  const uint16_t* bias;
+  void* C;
+  uint32_t* counters;        // split sums: arrivals per output tile
+  float* part;               // and partial sums
+  int M, N, K, out;
+};
+
+// E4M3 rows through fp16 products. The matrix cores' 8-bit products drop, in
+// each run of eight along k, what lies below 2^-13 of the largest (found by
+// adding 2^8 and 2^-6 on the instruction; fp4 x fp4 is exact, fp16 sums are float32):
+// 8e-6 of the norm of normal data, at worst 2^-10 of the sum of magnitudes.
+// That is below the rounding of an fp16 result on data that is not made for it;
+// a float32 result is summed from fp16 products, at a third of the rate.
+constexpr int MX_A8_EXACT = 3;
+constexpr bool mx_row8(int act) { return act == W4_MX_A8 || act == MX_A8_EXACT; }
+constexpr bool mx_half(int act) { return act == W4_MX_A16 || act == MX_A8_EXACT; }
+
+template <int ACT>
+constexpr int act_bytes(int k) {             // bytes of k elements of a row
+  return ACT == W4_MX_A16 ? 2 * k : mx_row8(ACT) ? k : k / 2;
+}
+
+// eight E4M3 codes as fp16 (exact)
+__device__ __forceinline__ h8 fp8_h8(uint32_t lo, uint32_t hi) {
+  const h2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+  const h2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+  const h2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+  const h2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+  return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// 16-byte chunks past a row's end are read from here: the packed weights are
+// zero there, but what lies behind a row may be a NaN
+__device__ __attribute__((aligned(16))) const uint8_t mx_zeros[16] = {0};
+
+int launch_mx_rows(int act, const MxParams& p, hipStream_t stream);
+int launch_mx_gemm(int act, const MxParams& p, hipStream_t stream);
+
+}  // namespace w4

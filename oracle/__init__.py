@@ -15,5 +15,7 @@ from .w4_oracle import *  # noqa: F401,F403
 from .w4_oracle import __all__  # noqa: F401
 from .layer_oracle import *  # noqa: F401,F403
 from .layer_oracle import __all__ as _layer_all
+from .mx_oracle import *  # noqa: F401,F403
+from .mx_oracle import __all__ as _mx_all
 
-__all__ = [*__all__, *_layer_all]
+__all__ = [*__all__, *_layer_all, *_mx_all]
