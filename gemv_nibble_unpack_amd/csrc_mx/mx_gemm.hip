@@ -1,12 +1,14 @@
 // Tiled product of many rows with MXFP4 weights.
 //
-// Four waves (2 along m, 2 along n) own a tile of 64 TM x 64 TN outputs, each 32 TM x
-// 32 TN of them on 32 x 32 matrix instructions: v_mfma_scale_f32_32x32x64_f8f6f4
-// for 4-bit and 8-bit rows (the one shape that multiplies 4-bit codes at twice
-// the rate of 8-bit ones), v_mfma_f32_32x32x16_f16 for fp16 rows, whose weights
-// widen in registers. Weights are the row operand, so a lane ends with runs of
-// four columns of C. Rows and weights come to LDS by direct loads, a ring of
-// NS stages.
+// Eight waves, WM along m and WN along n, own a tile of 32 TM WM x 32 TN WN
+// outputs, each 32 TM x 32 TN of them on 32 x 32 matrix instructions:
+// v_mfma_scale_f32_32x32x64_f8f6f4 for 4-bit and 8-bit rows (the one shape that
+// multiplies 4-bit codes at twice the rate of 8-bit ones), v_mfma_f32_32x32x16_f16
+// for fp16 rows, whose weights widen in registers. Weights are the row operand,
+// so a lane ends with runs of four columns of C. Rows, weights and scales come to
+// LDS by direct loads, a ring of NS stages of 128 k. A wave reads about 10 KB/us
+// however many loads it has in flight, so four waves of the same tiles were bound
+// by their loads.
 #include "mx_gemm.hpp"
 
 namespace w4 {
@@ -15,32 +17,32 @@ namespace w4 {
 // multiple of 4 scales long, aligned), or as pairs of aligned words shifted.
 enum { ROW_SCALES_NONE, ROW_SCALES_WORDS, ROW_SCALES_SHIFTED };
 
-template <int ACT, int TM, int TN, int NS_, int RS>
+template <int ACT, int WM_, int WN_, int TM_, int TN_, int NS_, int RS_>
 struct MxTile {
-  static constexpr int NS = NS_;
-  static constexpr int BM = 64 * TM, BN = 64 * TN, STRIPS = BN / 16;
-  static constexpr int TK = ACT == W4_MX_A16 ? 64 : 128;          // k of a stage
-  static constexpr int QS = 512 / TK;                             // stages of a quad of k tiles
-  static constexpr int RB = act_bytes<ACT>(TK);                   // bytes of a staged row
+  static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NS = NS_, RS = RS_;
+  static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+  static constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, STRIPS = BN / 16;
+  static constexpr int RB = act_bytes<ACT>(128);                  // bytes of a staged row
   static constexpr int CH = RB / 16;                              // and its 16-byte chunks
-  static constexpr int WB = 8 * TK;                               // bytes of a staged strip
-  static constexpr int A_BYTES = BM * RB, W_BYTES = STRIPS * WB;
+  static constexpr int A_BYTES = BM * RB, W_BYTES = STRIPS * TILE_BYTES;
   static constexpr int AS_BYTES = RS * BM * 4;                    // rows' scales
   static constexpr int STAGE = A_BYTES + W_BYTES + AS_BYTES;
-  static constexpr int A_LOADS = A_BYTES / 4096, W_LOADS = W_BYTES / 4096;   // a wave's, of 1 KiB
-  static constexpr int AS_LOADS = (RS * BM + 255) / 256;          // of 256 bytes
-  static constexpr int LOADS = A_LOADS + W_LOADS + AS_LOADS + 1;  // and one of weights' scales
-  static constexpr int WS_BYTES = STRIPS * 256;                   // weights' scales of a quad
+  // a wave's loads: rows and weights 1 KiB each, scales a word a lane
+  static constexpr int A_LOADS = A_BYTES / 1024 / WAVES, W_LOADS = W_BYTES / 1024 / WAVES;
+  static constexpr int AS_LOADS = (RS * BM + 64 * WAVES - 1) / (64 * WAVES);
+  static constexpr int LOADS = A_LOADS + W_LOADS + AS_LOADS + 1;
+  static constexpr int WS_BYTES = STRIPS * 256;                   // weights' scales of a quad of k tiles
   static constexpr int LDS = NS * STAGE + 2 * WS_BYTES;
-  static_assert(A_BYTES % 4096 == 0 && W_BYTES % 4096 == 0, "whole loads for each wave");
-  static_assert(STRIPS <= 4 * QS && NS <= QS, "a quad's scales come during the quad before");
+  static constexpr bool SPLIT = BM == 64;                     // may be split along k
+  static_assert(W_BYTES % (1024 * WAVES) == 0 && A_BYTES % (1024 * WAVES) == 0, "whole loads for each wave");
+  static_assert(STRIPS <= 4 * WAVES && NS <= 4, "a quad's scales come during the quad before");
   static_assert(LDS <= 160 * 1024, "LDS exceeds the CU");
 };
 
 // where chunk c of a staged row lies: rows of a fragment spread over the banks
 template <int CH>
 __device__ __forceinline__ int mx_chunk(int row, int c) {
-  return CH == 4 ? c ^ ((row >> 2) & 3) : c ^ ((row >> 1) & 7);
+  return CH == 4 ? c ^ ((row >> 2) & 3) : CH == 8 ? c ^ ((row >> 1) & 7) : c ^ (row & 15);
 }
 
 // operands of 64 k for a wave's row and column tiles
@@ -51,69 +53,65 @@ struct MxFrags {
 };
 
 // (a device function, so that the kernel's host stub holds no device assembly)
-template <int ACT, int TM, int TN, int NS_, int RS>
-__device__ __forceinline__ void mx_gemm_tile(const MxParams& p, int mblocks, int nblocks, int per_xcd) {
-  using S = MxTile<ACT, TM, TN, NS_, RS>;
+template <int ACT, typename S>
+__device__ __forceinline__ void mx_gemm_tile(const MxParams& p, int mblocks, int nblocks, int per_xcd,
+                                             int splits) {
+  constexpr int TM = S::TM, TN = S::TN, RS = S::RS;
   using F = MxFrags<ACT, TM, TN>;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int id = blockIdx.x, local = id >> 3;
   const int tix = (id & 7) * per_xcd + local;            // an XCD's tiles share their columns
-  if (local >= per_xcd || tix >= mblocks * nblocks) return;
-  const int nb = tix / mblocks, mb = tix - nb * mblocks;
+  if (local >= per_xcd || tix >= mblocks * nblocks * splits) return;
+  const int split = tix / (mblocks * nblocks), tile = tix - split * (mblocks * nblocks);
+  const int nb = tile / mblocks, mb = tile - nb * mblocks;
 
   const MxGeometry geo = mx_geometry(p.N, p.K);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = wave % S::WM, wn = wave / S::WM;
   const int l31 = lane & 31, half = lane >> 5;
   const int r = lane & 15, hi = (lane >> 4) & 1;         // this lane's weight row: strip 2 j + hi, row r
   const int m0 = mb * S::BM, t0 = nb * S::STRIPS;
   const int KB = p.K / 32;
-  const int nst = geo.KT * (128 / S::TK);
+  // this block's k tiles: whole quads
+  const int kt0 = 4 * (int)((int64_t)geo.KQ * split / splits);
+  const int kt1 = min(geo.KT, 4 * (int)((int64_t)geo.KQ * (split + 1) / splits));
   uint8_t* const wscales = smem + S::NS * S::STAGE;      // [2 quads][strip][64 lanes] words
 
   // ---- direct loads to LDS -------------------------------------------------------
-  // a sixteenth or more of quad q's weight scales: strips 4 piece .. (twice where there are fewer)
+  // a quarter of quad q's weight scales (all of them more than once where strips are few)
   auto issue_scales = [&](int q, int piece) {
-    const int strip = (4 * piece + wave) % S::STRIPS;
-    const int t = min(t0 + strip, geo.NT - 1);
+    const int strip = (piece * S::WAVES + wave) % S::STRIPS, t = min(t0 + strip, geo.NT - 1);
     __builtin_amdgcn_global_load_lds(
         p.Wp + geo.s_off + ((int64_t)t * geo.KQ + min(q, geo.KQ - 1)) * 256 + lane * 4,
         wscales + (q & 1) * S::WS_BYTES + strip * 256, 4, 0, 0);
   };
-  // load q of a stage: rows, weights, rows' scales
-  auto issue = [&](int st, int slot, int q) {
-    st = min(st, nst - 1);                               // past the end: again the last
+  // load q of k tile kt: rows, weights, rows' scales
+  auto issue = [&](int kt, int slot, int q) {
+    kt = min(kt, kt1 - 1);                               // past the end: again the last
     uint8_t* dst = smem + slot * S::STAGE;
     if (q < S::A_LOADS) {
-      constexpr int RPL = 64 / S::CH;                    // rows of a load
-      const int row = (wave * S::A_LOADS + q) * RPL + lane / S::CH;
+      const int first = (wave * S::A_LOADS + q) * 1024;
+      const int row = first / S::RB + lane / S::CH;
       const int c = mx_chunk<S::CH>(row, lane % S::CH);
-      const int k = st * S::TK + c * (S::TK / S::CH);
+      const int k = 128 * kt + c * (128 / S::CH);
       const uint8_t* src = p.A + (int64_t)min(m0 + row, p.M - 1) * act_bytes<ACT>(p.K) + act_bytes<ACT>(k);
-      __builtin_amdgcn_global_load_lds(k < p.K ? src : mx_zeros, dst + (wave * S::A_LOADS + q) * 1024,
-                                       16, 0, 0);
+      __builtin_amdgcn_global_load_lds(k < p.K ? src : mx_zeros, dst + first, 16, 0, 0);
     } else if (q < S::A_LOADS + S::W_LOADS) {
-      q -= S::A_LOADS;
-      constexpr int LPS = S::WB / 16;                    // lanes of a strip: 64 or 32
-      const int strip = (wave * S::W_LOADS + q) * (64 / LPS) + lane / LPS;
-      const int t = min(t0 + strip, geo.NT - 1);
-      const uint8_t* src = p.Wp + (int64_t)t * geo.KT * TILE_BYTES + (int64_t)st * S::WB + (lane % LPS) * 16;
-      __builtin_amdgcn_global_load_lds(src, dst + S::A_BYTES + (wave * S::W_LOADS + q) * 1024, 16, 0, 0);
+      const int strip = wave * S::W_LOADS + q - S::A_LOADS, t = min(t0 + strip, geo.NT - 1);
+      __builtin_amdgcn_global_load_lds(p.Wp + ((int64_t)t * geo.KT + kt) * TILE_BYTES + lane * 16,
+                                       dst + S::A_BYTES + strip * TILE_BYTES, 16, 0, 0);
     } else if constexpr (RS != ROW_SCALES_NONE) {
-      q -= S::A_LOADS + S::W_LOADS;
       // words [part][row]; shifted: the aligned words that a row's four scales lie in
-      const int item = ((q * 4 + wave) * 64 + lane) % (RS * S::BM);
+      const int base = ((q - S::A_LOADS - S::W_LOADS) * S::WAVES + wave) * 64 % (RS * S::BM), item = base + lane;
       const int row = min(m0 + item % S::BM, p.M - 1), part = item / S::BM;
-      uintptr_t src = (uintptr_t)(p.a_scales + (int64_t)row * KB + 4 * st);
+      uintptr_t src = (uintptr_t)(p.a_scales + (int64_t)row * KB + 4 * kt);
       if constexpr (RS == ROW_SCALES_SHIFTED) {
         const uintptr_t last = (uintptr_t)(p.a_scales + (int64_t)p.M * KB - 1) & ~(uintptr_t)3;
         src = (src & ~(uintptr_t)3) + 4 * part;
         src = src < last ? src : last;
       }
-      __builtin_amdgcn_global_load_lds((const void*)src,
-                                       dst + S::A_BYTES + S::W_BYTES + ((q * 4 + wave) * 256) % S::AS_BYTES,
-                                       4, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)src, dst + S::A_BYTES + S::W_BYTES + base * 4, 4, 0, 0);
     }
   };
 
@@ -172,12 +170,12 @@ __device__ __forceinline__ void mx_gemm_tile(const MxParams& p, int mblocks, int
   auto fetch = [&](F& f, int slot, int s, int q) {
     const uint8_t* a = smem + slot * S::STAGE;
     if (q < TN) {
-      const uint8_t* w = a + S::A_BYTES + (2 * wn * TN + hi) * S::WB + (half * 16 + r) * 16 + s * 512;
-      f.w[q] = *reinterpret_cast<const u4*>(w + 2 * q * S::WB);
+      const uint8_t* w = a + S::A_BYTES + (2 * wn * TN + hi) * TILE_BYTES + (half * 16 + r) * 16 + s * 512;
+      f.w[q] = *reinterpret_cast<const u4*>(w + 2 * q * TILE_BYTES);
     } else {
       const int i = (q - TN) / AF, x = (q - TN) % AF;
       const int row = 32 * (wm * TM + i) + l31;
-      const int c = ACT == W4_MX_A16    ? 4 * half + x
+      const int c = ACT == W4_MX_A16    ? 8 * s + 4 * half + x
                     : ACT == W4_MX_A8   ? 4 * s + 2 * x + half          // k 16 half .. and 32 + 16 half ..
                     : ACT == MX_A8_EXACT ? 4 * s + 2 * half + x
                                          : 2 * s + half;
@@ -238,29 +236,30 @@ __device__ __forceinline__ void mx_gemm_tile(const MxParams& p, int mblocks, int
 
   // Ring of NS stages. Every stage issues the same loads, so a fixed count waits
   // for the next stage's alone; the barrier publishes it and frees the stage that
-  // every wave has read out.
+  // every wave has read out. Weights' scales come a quarter with each stage of the
+  // quad before, into the half of their place that was read at its start.
   auto turn = [&] {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S::NS - 2) * S::LOADS) : "memory");
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
   auto next = [](int slot) { return slot + 1 == S::NS ? 0 : slot + 1; };
-  auto issue_item = [&](int st, int slot, int q) {
-    if (q < S::LOADS - 1) issue(st, slot, q);
-    else issue_scales(st / S::QS + 1, st % S::QS);
+  auto issue_item = [&](int kt, int slot, int q) {
+    if (q < S::LOADS - 1) issue(kt, slot, q);
+    else issue_scales((kt >> 2) + 1, kt & 3);
   };
 #pragma unroll
-  for (int q = 0; q < S::QS; ++q) issue_scales(0, q);
+  for (int q = 0; q < 4; ++q) issue_scales(kt0 >> 2, q);
 #pragma unroll
   for (int q = 0; q < S::NS; ++q)
 #pragma unroll
-    for (int x = 0; x < S::LOADS; ++x) issue_item(q, q, x);
+    for (int x = 0; x < S::LOADS; ++x) issue_item(kt0 + q, q, x);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S::NS - 1) * S::LOADS) : "memory");
   asm volatile("s_barrier" ::: "memory");
 
   // The operands of a step are read from LDS while the one before is multiplied.
   // `share` spreads n pieces of work evenly over the first `gaps` gaps.
   F f0, f1;
-  int slot = 0, st = 0;
+  int slot = 0;
 #pragma unroll
   for (int q = 0; q < FETCHES; ++q) fetch(f0, 0, 0, q);
 #pragma unroll
@@ -270,46 +269,85 @@ __device__ __forceinline__ void mx_gemm_tile(const MxParams& p, int mblocks, int
     for (int q = 0; q < n; ++q)
       if (h == (2 * q + 1) * gaps / (2 * n)) piece(q);
   };
-  // within the last step of stage st: the turn, then stage st + NS into its place
-  // and the next stage's first operands into `f`
-  auto advance = [&](int h, F& f) {
-    if (h == 0) {
-      __builtin_amdgcn_sched_barrier(0);
-      turn();
-    }
-    const int old = slot, now = next(slot);
-    constexpr int R = RS == ROW_SCALES_NONE ? 0 : TM;
-    share(h, GAPS - GAPS / 8, FETCHES + R, [&](int q) {
-      if (q < FETCHES) fetch(f, now, 0, q);
-      else read_row_scales(now, q - FETCHES);
-    });
-    share(h, GAPS, S::LOADS, [&](int q) { issue_item(st + S::NS, old, q); });
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  for (int kt = 0; kt < geo.KT; ++kt) {
+  constexpr int R = RS == ROW_SCALES_NONE ? 0 : TM;
+  for (int kt = kt0; kt < kt1; ++kt) {
     if ((kt & 3) == 0) quad_scales(kt >> 2);
     row_scales(kt);
-    if constexpr (S::TK == 64) {                         // two stages a k tile
-      multiply(f0, kt, 0, [&](int h) { advance(h, f1); });
-      slot = next(slot);
-      ++st;
-    } else {
-      multiply(f0, kt, 0, [&](int h) {
-        share(h, GAPS - GAPS / 8, FETCHES, [&](int q) { fetch(f1, slot, 1, q); });
+    multiply(f0, kt, 0, [&](int h) {
+      share(h, GAPS - GAPS / 8, FETCHES, [&](int q) { fetch(f1, slot, 1, q); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    // the turn, then k tile kt + NS into the place of this one and the next one's
+    // first operands
+    const int now = next(slot);
+    multiply(f1, kt, 1, [&](int h) {
+      if (h == 0) {
         __builtin_amdgcn_sched_barrier(0);
+        turn();
+      }
+      share(h, GAPS - GAPS / 8, FETCHES + R, [&](int q) {
+        if (q < FETCHES) fetch(f0, now, 0, q);
+        else read_row_scales(now, q - FETCHES);
       });
-    }
-    multiply(f1, kt, 1, [&](int h) { advance(h, f0); });
-    slot = next(slot);
-    ++st;
+      share(h, GAPS, S::LOADS, [&](int q) { issue_item(kt + S::NS, slot, q); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    slot = now;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // ---- split along k: the tile's last block adds the parts, in their order -----------
+  if constexpr (S::SPLIT) {
+    if (splits > 1) {
+      constexpr int PAIRS = TM * TN * 8, PT = PAIRS * 2 * S::THREADS;      // a thread's values in pairs; a part
+      uint32_t* part = reinterpret_cast<uint32_t*>(p.part) + (int64_t)tile * splits * PT + 2 * tid;
+      auto at = [&](int z, int x) { return part + (int64_t)z * PT + x * 2 * S::THREADS; };
+#pragma unroll
+      for (int x = 0; x < PAIRS; ++x) {
+        const f16v& a = acc[x / 8 / TN][x / 8 % TN];
+        dev_store2(at(split, x), __float_as_uint(a[x % 8 * 2]), __float_as_uint(a[x % 8 * 2 + 1]));
+      }
+      stores_done();
+      __syncthreads();
+      unsigned* flag = reinterpret_cast<unsigned*>(smem);
+      if (tid == 0) *flag = dev_arrive(p.counters + tile) == (unsigned)(splits - 1);
+      __syncthreads();
+      const bool last = *flag != 0;
+      __syncthreads();
+      if (!last) return;
+      if (tid == 0) dev_store(p.counters + tile, 0u);
+      // four parts' loads go out together: each is a round trip to the level that all XCDs share
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+      for (int z0 = 0; z0 < splits; z0 += 4) {
+        uint64_t v[4][PAIRS];
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+#pragma unroll
+          for (int x = 0; x < PAIRS; ++x) v[z][x] = dev_load2(at(min(z0 + z, splits - 1), x));
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          if (z0 + z >= splits) break;
+#pragma unroll
+          for (int x = 0; x < PAIRS; ++x) {
+            f16v& a = acc[x / 8 / TN][x / 8 % TN];
+            a[x % 8 * 2] += __uint_as_float((uint32_t)v[z][x]);
+            a[x % 8 * 2 + 1] += __uint_as_float((uint32_t)(v[z][x] >> 32));
+          }
+        }
+      }
+    }
+  }
 
   // ---- epilogue: lane holds row 32 (..) + l31, columns 8 (e >> 2) + 4 half + (e & 3) of
   // a tile. 32 rows at a time go through LDS, so that a row's columns are stored together.
   constexpr int WC = 32 * TN;                            // the wave's columns
   constexpr int PITCH = WC * 4 + 16;
-  static_assert(4 * 32 * PITCH <= S::NS * S::STAGE, "the staged rows lie in the ring");
+  static_assert(S::WAVES * 32 * PITCH <= S::NS * S::STAGE, "the staged rows lie in the ring");
   uint8_t* cw = smem + wave * 32 * PITCH;
   const int n0 = 16 * t0 + wn * WC;
   auto store = [&](auto half_out) {
@@ -378,43 +416,80 @@ __device__ __forceinline__ void mx_gemm_tile(const MxParams& p, int mblocks, int
   else store(std::false_type{});
 }
 
-template <int ACT, int TM, int TN, int NS, int RS>
-__global__ __launch_bounds__(256, 1) void k_mx_gemm(const MxParams p, int mblocks, int nblocks,
-                                                    int per_xcd) {
-  mx_gemm_tile<ACT, TM, TN, NS, RS>(p, mblocks, nblocks, per_xcd);
+template <int ACT, typename S>
+__global__ __launch_bounds__(S::THREADS, S::WAVES == 4 ? 1 : S::LDS > 80 * 1024 ? 2 : 4) void k_mx_gemm(const MxParams p, int mblocks,
+                                                                                  int nblocks, int per_xcd,
+                                                                                  int splits) {
+  mx_gemm_tile<ACT, S>(p, mblocks, nblocks, per_xcd, splits);
 }
 
-template <int ACT, int TM, int TN, int NS, int RS>
-int launch_tile(const MxParams& p, hipStream_t stream) {
-  using S = MxTile<ACT, TM, TN, NS, RS>;
-  const int mblocks = ceil_div(p.M, S::BM), nblocks = ceil_div(p.N, S::BN);
-  const int64_t tiles = (int64_t)mblocks * nblocks;
-  if (tiles > (1 << 23)) return W4_ERR_SHAPE;
-  const int per_xcd = (int)((tiles + 7) / 8);
-  allow_smem((const void*)&k_mx_gemm<ACT, TM, TN, NS, RS>, S::LDS);
-  hipLaunchKernelGGL((k_mx_gemm<ACT, TM, TN, NS, RS>), dim3(per_xcd * 8), dim3(256), S::LDS, stream, p,
-                     mblocks, nblocks, per_xcd);
+// The tile and the split along k, from the sizes (and not from the result's type,
+// which mx4_workspace_bytes does not know).
+struct MxPlan {
+  int bm, bn, splits;
+  int64_t tiles;
+  size_t ws;
+};
+static MxPlan mx_plan(int act, int M, int N, int K) {
+  // The tile by the most that a CU gets of it, in units of a 256 x 256 tile's time
+  // (100). 8-bit rows, us, 256 x 256, 128 x 256, 128 x 128, 64 x 128: 2048 x 8192 x
+  // 4096 76, 83, 80, 105; 2048 x 4096 x 11008 116, 84, 91, 124; 777 x 4096 x 4096
+  // 44, 28, 21.5, 21.0; 200 x 4096 x 4096 43, 25, 19, 14.5. fp16 rows have no 256 x
+  // 256 tile, whose stages would not fit.
+  const int bms[4] = {256, 128, 128, 64}, bns[4] = {256, 256, 128, 128}, each[4] = {100, 60, 34, 22};
+  MxPlan best{};
+  int64_t least = INT64_MAX;
+  for (int x = act == W4_MX_A16; x < 4; ++x) {
+    const int64_t tiles = (int64_t)ceil_div(M, bms[x]) * ceil_div(N, bns[x]);
+    const int64_t cost = (tiles + 255) / 256 * each[x];
+    if (cost < least) least = cost, best = MxPlan{bms[x], bns[x], 1, tiles, 0};
+  }
+  // The smallest tile where it leaves CUs without work: splits along k, of whole quads
+  // of k tiles. A k tile takes 0.55, 0.3 or 0.26 us (fp16, 8-bit, 4-bit rows), the
+  // exchange about 3 us and 0.017 for each block: 45 x 3200 x 8640, 8-bit rows, 26 us
+  // whole, 14.7 in 4, 15.3 in 8; 200 x 4096 x 4096, fp16, 30 whole, 25 in 2 or 4.
+  if (best.bm == 64 && best.tiles < 256) {
+    const int KT = (K + 127) / 128, KQ = (KT + 3) / 4;
+    const double t = act == W4_MX_A16 ? 0.55 : act == W4_MX_A8 ? 0.3 : 0.26;
+    double least_us = t * KT;
+    for (int s = 2; s <= min(KQ, 8); ++s) {
+      const double us = t * 4 * ((KQ + s - 1) / s) + 3 + 0.017 * best.tiles * s;
+      if (us < least_us) least_us = us, best.splits = s;
+    }
+  }
+  if (best.splits > 1) best.ws = WS_COUNTERS + (size_t)(best.tiles * best.splits * best.bm * best.bn * 4);
+  return best;
+}
+
+template <int ACT, typename S>
+int launch_tile(const MxParams& p, const MxPlan& plan, hipStream_t stream) {
+  const int64_t blocks = plan.tiles * plan.splits;
+  if (blocks > (1 << 22)) return W4_ERR_SHAPE;
+  const int per_xcd = (int)((blocks + 7) / 8);
+  allow_smem((const void*)&k_mx_gemm<ACT, S>, S::LDS);
+  hipLaunchKernelGGL((k_mx_gemm<ACT, S>), dim3(per_xcd * 8), dim3(S::THREADS), S::LDS, stream, p,
+                     ceil_div(p.M, S::BM), ceil_div(p.N, S::BN), per_xcd, plan.splits);
   return launch_status();
 }
 
-// The tile by the most that a CU gets of it, in units of a 256 x 256 tile's time (100):
-// a 128 x 256 one costs 60 of it (4-bit rows 65), a 128 x 128 one 34 (46), a 64 x 128
-// one 22 (32). 2048 rows (8-bit, us): N = 8192, K = 4096 67, 74, 81 for the first
-// three; N = 4096, K = 11008 108, 73, 88; 777 rows, N = K = 4096 44, 28, 21.
+// Stages: what the CU's LDS holds, two blocks of it for the smaller tiles. fp16 rows
+// take eight waves (2048 x 11008 x 4096 185 us, 205 on four; 777 x 4096 x 4096 36,
+// 42), which hide the widening of the weights, 8-bit and 4-bit rows four (2048 x
+// 8192 x 4096 67 and 50 us, 93 and 52 on eight).
 template <int ACT, int RS>
 int launch_gemm(const MxParams& p, hipStream_t stream) {
-  constexpr bool A4 = ACT == W4_MX_A4;
-  auto cost = [&](int bm, int bn, int each) {
-    const int64_t tiles = (int64_t)ceil_div(p.M, bm) * ceil_div(p.N, bn);
-    return (tiles + 255) / 256 * each;
-  };
-  const int64_t c[4] = {cost(256, 256, 100), cost(128, 256, A4 ? 65 : 60), cost(128, 128, A4 ? 46 : 34),
-                        cost(64, 128, A4 ? 32 : 22)};
-  const int64_t least = min(min(c[0], c[1]), min(c[2], c[3]));
-  if (least == c[0]) return launch_tile<ACT, 4, 4, A4 ? 4 : 3, RS>(p, stream);
-  if (least == c[1]) return launch_tile<ACT, 2, 4, A4 ? 4 : 3, RS>(p, stream);
-  if (least == c[2]) return launch_tile<ACT, 2, 2, A4 ? 4 : 3, RS>(p, stream);
-  return launch_tile<ACT, 1, 2, 4, RS>(p, stream);
+  const MxPlan plan = mx_plan(ACT == MX_A8_EXACT ? W4_MX_A8 : ACT, p.M, p.N, p.K);
+  if constexpr (ACT == W4_MX_A16) {
+    if (plan.bn == 256) return launch_tile<ACT, MxTile<ACT, 2, 4, 2, 2, 3, RS>>(p, plan, stream);
+    if (plan.bm == 128) return launch_tile<ACT, MxTile<ACT, 2, 4, 2, 1, 3, RS>>(p, plan, stream);
+    return launch_tile<ACT, MxTile<ACT, 2, 4, 1, 1, 3, RS>>(p, plan, stream);
+  } else {
+    constexpr int NS = ACT == W4_MX_A4 ? 4 : 3;
+    if (plan.bm == 256) return launch_tile<ACT, MxTile<ACT, 2, 2, 4, 4, NS, RS>>(p, plan, stream);
+    if (plan.bn == 256) return launch_tile<ACT, MxTile<ACT, 2, 2, 2, 4, 4, RS>>(p, plan, stream);
+    if (plan.bm == 128) return launch_tile<ACT, MxTile<ACT, 2, 2, 2, 2, NS, RS>>(p, plan, stream);
+    return launch_tile<ACT, MxTile<ACT, 2, 2, 1, 2, 4, RS>>(p, plan, stream);
+  }
 }
 
 int launch_mx_gemm(int act, const MxParams& p, hipStream_t stream) {
@@ -430,7 +505,11 @@ int launch_mx_gemm(int act, const MxParams& p, hipStream_t stream) {
 
 using namespace w4;
 
-static constexpr int ROWS_MOST = 64;
+// Few rows stream the weights. 33 to 64 rows: up to 768 strips (N = 12288), three a CU:
+// 64 x 11008 x 4096 rows 24.6, 13.0, 13.5 us (fp16, 8-bit, 4-bit), tiles 22.6, 14.6,
+// 13.7; 64 x 4096 x 4096 18.8, 10.5, 10.3 and 17, 12, 12; 64 x 22016 x 4096 45, 25, 27
+// and 24, 15, 14.
+static bool few_rows(int M, int N) { return M <= 32 || (M <= 64 && N <= 768 * 16); }
 
 static bool mx_gemm_sizes_ok(int M, int N, int K) {
   return M >= 0 && M <= (1 << 30) && prepack_mx4_bytes(N, K) != 0;
@@ -438,7 +517,7 @@ static bool mx_gemm_sizes_ok(int M, int N, int K) {
 
 extern "C" size_t mx4_workspace_bytes(int op, int M, int N, int K) {
   if (op < W4_MX_A16 || op > W4_MX_A4 || !mx_gemm_sizes_ok(M, N, K) || M == 0) return 0;
-  return 0;
+  return few_rows(M, N) ? 0 : mx_plan(op, M, N, K).ws;
 }
 
 static int mx_gemm(int act, MxParams p, void* workspace, size_t workspace_bytes, hipStream_t stream) {
@@ -454,7 +533,7 @@ static int mx_gemm(int act, MxParams p, void* workspace, size_t workspace_bytes,
   if (need > 0 && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;
   p.counters = (uint32_t*)workspace;
   p.part = workspace ? (float*)((uint8_t*)workspace + WS_COUNTERS) : nullptr;
-  return p.M <= ROWS_MOST ? launch_mx_rows(act, p, stream) : launch_mx_gemm(act, p, stream);
+  return few_rows(p.M, p.N) ? launch_mx_rows(act, p, stream) : launch_mx_gemm(act, p, stream);
 }
 
 extern "C" int mx4a16_gemm(const uint16_t* A, const uint8_t* Wp, const uint16_t* bias, void* C,

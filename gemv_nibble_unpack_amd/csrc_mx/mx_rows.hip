@@ -8,16 +8,22 @@
 
 namespace w4 {
 
-template <int ACT>
-struct RowFrag {
-  h8 h[mx_half(ACT) ? 4 : 1];
-  v8i q;
-  uint32_t s;
+// operands of one k tile: SP strips of weights, QT column operands of rows
+template <int ACT, int QT, int SP>
+struct RowTile {
+  u4 w[SP];
+  uint32_t s[SP];                          // the weights' scale
+  u4 a[QT][ACT == W4_MX_A16 ? 4 : mx_row8(ACT) ? 2 : 1];
+  uint32_t as[QT];                         // A4: the rows' scales
 };
 
-template <int ACT, int QT, int SP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_mx_rows(const MxParams p) {
+constexpr int ROW_WAVES = 8;
+
+template <int ACT, int QT, int SP>
+__global__ __launch_bounds__(64 * ROW_WAVES) void k_mx_rows(const MxParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  using T = RowTile<ACT, QT, SP>;
+  constexpr int WAVES = ROW_WAVES;
   const MxGeometry geo = mx_geometry(p.N, p.K);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -51,68 +57,83 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_rows(const MxParams p) {
   auto chunk = [&](const uint8_t* r, int k) {          // 16 bytes of a row at element k
     return *reinterpret_cast<const u4*>(k < p.K ? r + act_bytes<ACT>(k) : mx_zeros);
   };
-  auto load_a = [&](int u, int kt, RowFrag<ACT>& f) {
-    if constexpr (ACT == W4_MX_A16) {
+  auto load = [&](int kt, T& f) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        f.h[j] = __builtin_bit_cast(h8, chunk(row[u], 128 * kt + 32 * g + 8 * j));
-    } else if constexpr (ACT == MX_A8_EXACT) {
+    for (int i = 0; i < SP; ++i) {
+      f.w[i] = *reinterpret_cast<const u4*>(wt[i] + (int64_t)kt * TILE_BYTES);
+      f.s[i] = ws[i][(kt >> 2) * 256 + (kt & 3)];
+    }
+    const int k = 128 * kt;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const u4 a = chunk(row[u], 128 * kt + 32 * g + 16 * j);
-        f.h[2 * j] = fp8_h8(a[0], a[1]);
-        f.h[2 * j + 1] = fp8_h8(a[2], a[3]);
+    for (int u = 0; u < QT; ++u) {
+      if constexpr (ACT == W4_MX_A16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f.a[u][j] = chunk(row[u], k + 32 * g + 8 * j);
+      } else if constexpr (ACT == MX_A8_EXACT) {
+        f.a[u][0] = chunk(row[u], k + 32 * g), f.a[u][1] = chunk(row[u], k + 32 * g + 16);
+      } else if constexpr (ACT == W4_MX_A8) {            // k 16 g .. and 64 + 16 g ..
+        f.a[u][0] = chunk(row[u], k + 16 * g), f.a[u][1] = chunk(row[u], k + 64 + 16 * g);
+      } else {
+        f.a[u][0] = chunk(row[u], k + 32 * g);
+        f.as[u] = *(k + 32 * g < p.K ? srow[u] + 4 * kt + g : mx_zeros);
       }
-    } else if constexpr (ACT == W4_MX_A8) {            // k 16 g .. and 64 + 16 g ..
-      const u4 a = chunk(row[u], 128 * kt + 16 * g), b = chunk(row[u], 128 * kt + 64 + 16 * g);
-      f.q = v8i{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-    } else {
-      const u4 a = chunk(row[u], 128 * kt + 32 * g);
-      f.q = v8i{(int)a[0], (int)a[1], (int)a[2], (int)a[3]};
-      f.s = *(128 * kt + 32 * g < p.K ? srow[u] + 4 * kt + g : mx_zeros);
     }
   };
-  auto product = [&](const u4 w, uint32_t s, uint32_t top, const RowFrag<ACT>& f, f4 d) {
+  auto multiply = [&](const T& f) {
     if constexpr (mx_half(ACT)) {
-      const float up = h_scale(s, top);
+      h8 a[QT][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp4_h8(w[j], up), f.h[j], d, 0, 0, 0);
-      return d;
+      for (int u = 0; u < QT; ++u) {
+        if constexpr (ACT == W4_MX_A16) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) a[u][x] = __builtin_bit_cast(h8, f.a[u][x]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) a[u][x] = fp8_h8(f.a[u][x / 2][2 * (x & 1)], f.a[u][x / 2][2 * (x & 1) + 1]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < SP; ++i) {
+        const float up = h_scale(f.s[i], rowmax[i]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const h8 b = fp4_h8(f.w[i][x], up);
+#pragma unroll
+          for (int u = 0; u < QT; ++u)
+            acc[i][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, a[u][x], acc[i][u], 0, 0, 0);
+        }
+      }
     } else {
-      const v8i a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-      if constexpr (ACT == W4_MX_A8)
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, f.q, d, 4, 0, 0, s, 0, 127);
-      else
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, f.q, d, 4, 4, 0, s, 0, f.s);
+#pragma unroll
+      for (int i = 0; i < SP; ++i) {
+        const v8i b = {(int)f.w[i][0], (int)f.w[i][1], (int)f.w[i][2], (int)f.w[i][3]};
+#pragma unroll
+        for (int u = 0; u < QT; ++u) {
+          const u4 x = f.a[u][0];
+          if constexpr (ACT == W4_MX_A8) {
+            const u4 y = f.a[u][1];
+            const v8i a = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+            acc[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc[i][u], 4, 0, 0, f.s[i], 0, 127);
+          } else {
+            const v8i a = {(int)x[0], (int)x[1], (int)x[2], (int)x[3]};
+            acc[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc[i][u], 4, 4, 0, f.s[i], 0, f.as[u]);
+          }
+        }
+      }
     }
   };
 
-  constexpr int U = 4 / SP;
-  int kt = geo.KT * wave / WAVES;
+  // U tiles' loads together (a second set in flight meanwhile takes registers, so
+  // resident waves: one fp16 row, N = 11008, K = 4096 8.0 -> 11.9 us)
+  constexpr int U = SP >= 3 ? 1 : SP == 2 ? 2 : 4;
   const int end = geo.KT * (wave + 1) / WAVES;
-  for (; kt < end; kt += U) {
-    u4 w[U][SP];
-    uint32_t s[U][SP];
+  for (int kt = geo.KT * wave / WAVES; kt < end; kt += U) {
+    T f[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) load(min(kt + j, end - 1), f[j]);
 #pragma unroll
     for (int j = 0; j < U; ++j)
-#pragma unroll
-      for (int i = 0; i < SP; ++i) {
-        const int x = min(kt + j, end - 1);
-        w[j][i] = *reinterpret_cast<const u4*>(wt[i] + (int64_t)x * TILE_BYTES);
-        s[j][i] = ws[i][(x >> 2) * 256 + (x & 3)];
-      }
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if (kt + j >= end) break;
-#pragma unroll
-      for (int u = 0; u < QT; ++u) {
-        RowFrag<ACT> f;
-        load_a(u, kt + j, f);
-#pragma unroll
-        for (int i = 0; i < SP; ++i) acc[i][u] = product(w[j][i], s[j][i], rowmax[i], f, acc[i][u]);
-      }
-    }
+      if (kt + j < end) multiply(f[j]);
   }
 
   // ---- the waves' sums ------------------------------------------------------
@@ -149,19 +170,42 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_rows(const MxParams p) {
 }
 
 template <int ACT, int QT, int SP>
-int launch_rows(const MxParams& p, hipStream_t stream) {
-  constexpr int WAVES = 8, lds = WAVES * SP * QT * 1024;
-  allow_smem((const void*)&k_mx_rows<ACT, QT, SP, WAVES>, lds);
-  hipLaunchKernelGGL((k_mx_rows<ACT, QT, SP, WAVES>), grid_of(((int64_t)p.N + 16 * SP - 1) / (16 * SP)),
-                     dim3(64 * WAVES), lds, stream, p);
+int launch_rows_sp(const MxParams& p, hipStream_t stream) {
+  constexpr int lds = ROW_WAVES * SP * QT * 1024;
+  allow_smem((const void*)&k_mx_rows<ACT, QT, SP>, lds);
+  hipLaunchKernelGGL((k_mx_rows<ACT, QT, SP>), grid_of(((int64_t)p.N + 16 * SP - 1) / (16 * SP)),
+                     dim3(64 * ROW_WAVES), lds, stream, p);
   return launch_status();
+}
+
+// Strips a block: rounds of blocks over the 256 CUs times what a block reads for a k
+// tile, SP KiB of weights and the rows. N = 11008, K = 4096, us for 1, 2, 3, 4 strips:
+// 27 fp16 rows 24.0, 18.7, 12.1, 13.4, one 4-bit row 5.0, 6.2, 4.9, 5.7; N = 4096: 16
+// 8-bit rows 4.9, 5.8, 6.3, 7.1.
+template <int ACT, int QT>
+int launch_rows(const MxParams& p, hipStream_t stream) {
+  const int strips = ceil_div(p.N, 16);
+  const double rows = p.M * act_bytes<ACT>(128) / 1024.0;
+  int best = 1;
+  double least = 1e30;
+  for (int sp = 1; sp <= 4; ++sp) {
+    const double cost = ceil_div(ceil_div(strips, sp), 256) * (sp + rows);
+    if (cost < least) least = cost, best = sp;
+  }
+  switch (best) {
+    case 1: return launch_rows_sp<ACT, QT, 1>(p, stream);
+    case 2: return launch_rows_sp<ACT, QT, 2>(p, stream);
+    case 3: return launch_rows_sp<ACT, QT, 3>(p, stream);
+    default: return launch_rows_sp<ACT, QT, 4>(p, stream);
+  }
 }
 
 template <int ACT>
 int launch_rows_act(const MxParams& p, hipStream_t stream) {
-  if (p.M <= 16) return launch_rows<ACT, 1, 1>(p, stream);
-  if (p.M <= 32) return launch_rows<ACT, 2, 1>(p, stream);
-  return launch_rows<ACT, 4, 1>(p, stream);
+  if (p.M <= 16) return launch_rows<ACT, 1>(p, stream);
+  if (p.M <= 32) return launch_rows<ACT, 2>(p, stream);
+  if (p.M <= 48) return launch_rows<ACT, 3>(p, stream);
+  return launch_rows<ACT, 4>(p, stream);
 }
 
 int launch_mx_rows(int act, const MxParams& p, hipStream_t stream) {

@@ -4,7 +4,8 @@
  * weights, and a mixture-of-experts layer on them. Same library, status codes
  * and conventions as gemv_nibble_unpack.h (device pointers, caller-owned
  * buffers, asynchronous on `stream`, nothing allocated, nothing synchronised,
- * every argument checked before a launch); what differs is said here.
+ * every argument checked before a launch); what differs is said here. M and N are
+ * at most 2^30.
  *
  * The format (OCP microscaling, MXFP4)
  * ------------------------------------
@@ -95,8 +96,8 @@ int unprepack_mx4(const uint8_t* Wp, int N, int K, uint8_t* codes, uint8_t* scal
  * largest in their row of W, rounded to 2^-36 of the largest below that.
  * A block with scale 255 makes every sum that meets it NaN, as a NaN or
  * infinity of A does for its row.
- * Every M is served (M = 0 returns W4_OK without a launch): up to 64 rows a kernel that streams the weights, above
- * that a tiled product. Large buffers 16-byte aligned, a_scale its 4 bytes,
+ * Every M is served (M = 0 returns W4_OK without a launch): few rows by a
+ * kernel that streams the weights, more by a tiled product. Large buffers 16-byte aligned, a_scale its 4 bytes,
  * a_scales any address. Workspace: mx4_workspace_bytes(op, M, N, K) bytes (0 if
  * none is needed or an argument is invalid), the rules of w4_workspace_bytes.
  * Errors: W4_ERR_ARG (out_dtype), W4_ERR_SHAPE, W4_ERR_NULL, W4_ERR_ALIGN,
