@@ -1,18 +1,28 @@
 // A mixture-of-experts layer on MXFP4 weights for a few tokens.
 //
 // A (token, choice) is a pair. Two kernels: the first finds each token's experts
-// and writes h = act(gate) * up of every pair, the second multiplies by the
+// and writes h = w * act(gate) * up of every pair, the second multiplies by the
 // down projections and sums a token's pairs. Up to ROUTE_IN tokens every block of the
 // first kernel takes the choices itself, above that a kernel before it does.
+//
+// fp16 x meets the weights widened to fp16 (mx_common.hpp). h, a product of two
+// sums, has float32's range: it is kept as two bfloat16 numbers, hi + lo (16 bits
+// of it, relative error 2^-17), each multiplied by the weights, which are exact in
+// bfloat16, with float32 sums.
 //
 // Bound: the bytes of the experts in use.
 #include "mx_gemm.hpp"
 
 namespace w4 {
 
+typedef __bf16 b2v __attribute__((ext_vector_type(2)));
+typedef __bf16 b4v __attribute__((ext_vector_type(4)));
+typedef __bf16 b8v __attribute__((ext_vector_type(8)));
+
 constexpr int MOE_PAIRS = W4_MOE_MAX_TOKENS * W4_MOE_MAX_TOP;
-constexpr int ROUTE_IN = 8;
-constexpr int MOE_THREADS = 512, MOE_WAVES = 8;
+constexpr int ROUTE_IN = 4;
+constexpr int MOE_COLS = 16;             // tokens that the second kernel takes as columns
+constexpr int MOE_THREADS = 512, MOE_WAVES = 8, ROUTE_THREADS = 1024;
 constexpr int DOWN_SP = 4;               // strips of a block that takes one expert
 
 // which experts are in use and by whom
@@ -23,6 +33,7 @@ struct MoeRoute {
   int first[W4_MOE_MAX_EXPERTS + 1];     // of its pairs in `list`
   int list[MOE_PAIRS];                   // pairs token * top + choice, by expert
   float weight[MOE_PAIRS];               // of pair; -1: a choice that is none
+  int16_t column[MOE_COLS * W4_MOE_MAX_TOP][MOE_COLS];   // of expert in use and token: its pair, or -1
 };
 
 struct MoeParams {
@@ -32,13 +43,16 @@ struct MoeParams {
   uint16_t* out;
   uint32_t* counters;
   MoeRoute* route;
-  float *h, *y;                          // [pairs][I], [pairs][H]
+  __bf16* h;                             // hi [pairs][I], then lo
+  float* y;                              // [pairs][H]
   int T, H, I, E, top, act, renorm, half_logits;
 };
 
 struct MoeChoice {                       // in LDS while the choices are taken
   int id[MOE_PAIRS];                     // expert, -1 for none
-  int waves[MOE_WAVES];
+  int place[MOE_PAIRS];                  // among the expert's pairs
+  int count[W4_MOE_MAX_EXPERTS], before[W4_MOE_MAX_EXPERTS];
+  int waves[2][ROUTE_THREADS / 64];
 };
 
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -46,10 +60,10 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One wave: the `top` largest logits of token t, ties to the lowest expert, and
-// their softmax weights.
-__device__ void route_token(const MoeParams& p, int t, MoeRoute& r, MoeChoice& ch) {
-  constexpr int R = W4_MOE_MAX_EXPERTS / 64;
+// One wave: the `top` largest logits of token t (of up to 64 R experts), ties to the
+// lowest expert, and their softmax weights.
+template <int R>
+__device__ __forceinline__ void route_token(const MoeParams& p, int t, MoeRoute& r, MoeChoice& ch) {
   const int lane = threadIdx.x & 63;
   const float ninf = -__builtin_inff();
   float v[R];
@@ -66,81 +80,101 @@ __device__ void route_token(const MoeParams& p, int t, MoeRoute& r, MoeChoice& c
     key[i] = e < p.E ? order_key(v[i]) : 0u;
   }
   bad = __ballot(bad) != 0;
-  float most = 0.f, sum = 0.f;
+  // lane j keeps choice j
+  int id = -1;
+  float l = ninf, most = 0.f;
   for (int j = 0; j < p.top; ++j) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) m = max(m, key[i]);
     m = wave_max_u(m);
-    int id = -1;
+    int e = 0;
 #pragma unroll
     for (int i = R - 1; i >= 0; --i) {
       const uint64_t b = __ballot(key[i] == m);
-      if (b) id = 64 * i + __builtin_ctzll(b);
+      if (b) e = 64 * i + __builtin_ctzll(b);
     }
-    const float l = __uint_as_float(m & 0x80000000u ? m & 0x7FFFFFFFu : ~m);
-    const bool none = bad || m == 0 || l == ninf;
+    const float lj = __uint_as_float(m & 0x80000000u ? m & 0x7FFFFFFFu : ~m);
+    if (bad || m == 0 || lj == ninf) break;              // the same for the wave
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (id == 64 * i + lane) key[i] = 0;
-    if (j == 0) {
-      most = l;
-      if (!p.renorm && !none) {
-        float s = 0.f;
+      if (e == 64 * i + lane) key[i] = 0;
+    if (j == 0) most = lj;
+    if (lane == j) id = e, l = lj;
+  }
+  const float w = id >= 0 ? expf(l - most) : 0.f;
+  float s = w;
+  if (!p.renorm && !bad) {
+    s = 0.f;
 #pragma unroll
-        for (int i = 0; i < R; ++i) s += expf(v[i] - most);        // of -infinity: 0
-        sum = wave_sum_f(s);
-      }
-    }
-    const float w = none ? 0.f : expf(l - most);
-    if (p.renorm) sum += w;
-    if (lane == 0) {
-      ch.id[t * p.top + j] = none ? -1 : id;
-      r.weight[t * p.top + j] = none ? -1.f : w;
-    }
+    for (int i = 0; i < R; ++i) s += v[i] == ninf ? 0.f : expf(v[i] - most);
   }
-  if (lane == 0) {
-    r.bad[t] = bad;
-    for (int j = 0; j < p.top; ++j)
-      if (ch.id[t * p.top + j] >= 0) r.weight[t * p.top + j] /= sum;
+  s = wave_sum_f(s);
+  if (lane < p.top) {
+    ch.id[t * p.top + lane] = id;
+    r.weight[t * p.top + lane] = id >= 0 ? w / s : -1.f;
   }
+  if (lane == 0) r.bad[t] = bad;
 }
 
-// The whole block: experts in use and their pairs, from the choices.
-__device__ void route_lists(const MoeParams& p, MoeRoute& r, MoeChoice& ch) {
-  const int pairs = p.T * p.top, e = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int n = 0, before = 0;
-  if (e < p.E)
-    for (int i = 0; i < pairs; ++i) {
-      const int id = ch.id[i];
-      n += id == e;
-      before += id >= 0 && id < e;                       // their pairs come first
-    }
-  const uint64_t used = __ballot(n > 0);
-  if (lane == 0) ch.waves[wave] = __builtin_popcountll(used);
+// The whole block: experts in use and their pairs, from the choices. An expert's
+// pairs come in any order: they are columns of its products, none meets another.
+template <int THREADS>
+__device__ __forceinline__ void route_lists(const MoeParams& p, MoeRoute& r, MoeChoice& ch) {
+  const int pairs = p.T * p.top, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < pairs; i += THREADS)
+    if (ch.id[i] >= 0) ch.place[i] = atomicAdd(&ch.count[ch.id[i]], 1);
   __syncthreads();
-  int a = __builtin_popcountll(used & ((1ull << lane) - 1)), all = 0;
-  for (int i = 0; i < MOE_WAVES; ++i) {
-    if (i < wave) a += ch.waves[i];
-    all += ch.waves[i];
+  const int n = tid < p.E ? ch.count[tid] : 0;
+  const uint64_t used = __ballot(n > 0);
+  int upto = n;                                          // pairs of this expert and those before
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int q = __shfl_up(upto, o, 64);
+    if (lane >= o) upto += q;
+  }
+  if (lane == 63) {
+    ch.waves[0][wave] = __builtin_popcountll(used);
+    ch.waves[1][wave] = upto;
+  }
+  __syncthreads();
+  int a = __builtin_popcountll(used & ((1ull << lane) - 1)), all = 0, sum = 0;
+  upto -= n;
+  for (int i = 0; i < THREADS / 64; ++i) {
+    if (i < wave) a += ch.waves[0][i], upto += ch.waves[1][i];
+    all += ch.waves[0][i], sum += ch.waves[1][i];
   }
   if (n > 0) {
-    r.expert[a] = e;
-    r.first[a] = before;
-    int at = before;
-    for (int i = 0; i < pairs; ++i)
-      if (ch.id[i] == e) r.list[at++] = i;
-    if (a == all - 1) r.first[all] = at;
+    r.expert[a] = tid;
+    r.first[a] = upto;
+    ch.before[tid] = upto;
+    ch.count[tid] = a;
   }
-  if (threadIdx.x == 0) r.active = all;
+  if (tid == 0) r.active = all, r.first[all] = sum;
+  const bool columns = p.T <= MOE_COLS;
+  if (columns)
+    for (int i = tid; i < all * MOE_COLS / 2; i += THREADS) reinterpret_cast<uint32_t*>(r.column)[i] = 0xFFFFFFFFu;
+  __syncthreads();
+  for (int i = tid; i < pairs; i += THREADS)
+    if (ch.id[i] >= 0) {
+      r.list[ch.before[ch.id[i]] + ch.place[i]] = i;
+      if (columns) r.column[ch.count[ch.id[i]]][i / p.top] = (int16_t)i;
+    }
   __syncthreads();
 }
 
-__global__ __launch_bounds__(MOE_THREADS) void k_moe_route(const MoeParams p) {
-  __shared__ MoeChoice ch;
-  for (int t = threadIdx.x >> 6; t < p.T; t += MOE_WAVES) route_token(p, t, *p.route, ch);
+template <int R, int THREADS>
+__device__ __forceinline__ void route(const MoeParams& p, MoeRoute& r, MoeChoice& ch) {
+  if (threadIdx.x < W4_MOE_MAX_EXPERTS) ch.count[threadIdx.x] = 0;
+  for (int t = threadIdx.x >> 6; t < p.T; t += THREADS / 64) route_token<R>(p, t, r, ch);
   __syncthreads();
-  route_lists(p, *p.route, ch);
+  route_lists<THREADS>(p, r, ch);
+}
+
+template <int R>
+__global__ __launch_bounds__(ROUTE_THREADS) void k_moe_route(const MoeParams p) {
+  __shared__ MoeChoice ch;
+  route<R, ROUTE_THREADS>(p, *p.route, ch);
 }
 
 __device__ __forceinline__ float moe_act(float g, int act) {
@@ -152,281 +186,312 @@ __device__ __forceinline__ float moe_act(float g, int act) {
   return g / (1.f + expf(-z));           // tanh(z) = 2 / (1 + exp(-2 z)) - 1
 }
 
-// h of one strip of 16 inner rows (gate and up) for one expert's pairs
-template <int QT, bool ROUTE>
+// h of P strips of 16 inner rows (gate and up) for one expert's pairs, 16 QT of them at
+// a time. R: the block takes the choices itself (of up to 64 R experts); 0: they are there.
+template <int P, int QT, int R>
 __global__ __launch_bounds__(MOE_THREADS) void k_moe_up(const MoeParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];     // sums
-  __shared__ typename std::conditional<ROUTE, MoeRoute, int>::type own;
-  __shared__ typename std::conditional<ROUTE, MoeChoice, int>::type ch;
+  __shared__ typename std::conditional<R != 0, MoeRoute, int>::type own;
+  __shared__ typename std::conditional<R != 0, MoeChoice, int>::type ch;
+  constexpr int SP = 2 * P;              // strips: gate, up, gate, up ..
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int strips = p.I / 16;
-  const int a = block_number() / strips, s = block_number() - a * strips;
+  const int strips = p.I / 16, groups = (strips + P - 1) / P;
+  const int a = block_number() / groups, s0 = (block_number() - a * groups) * P;
   const MoeRoute* r = p.route;
-  if constexpr (ROUTE) {
-    if (wave < p.T) route_token(p, wave, own, ch);
-    __syncthreads();
-    route_lists(p, own, ch);
+  if constexpr (R != 0) {
+    route<R, MOE_THREADS>(p, own, ch);
     if (block_number() == 0)                             // for the second kernel
       for (int i = threadIdx.x; i < (int)(sizeof(MoeRoute) / 4); i += MOE_THREADS)
         reinterpret_cast<int*>(p.route)[i] = reinterpret_cast<const int*>(&own)[i];
     r = &own;
   }
-  if (a >= r->active) return;
-  const int e = r->expert[a], first = r->first[a], n = r->first[a + 1] - first;
+  const int active = r->active;
+  const int e = r->expert[min(a, W4_MOE_MAX_EXPERTS - 1)], first = r->first[min(a, W4_MOE_MAX_EXPERTS - 1)];
+  const int end_pair = r->first[min(a + 1, W4_MOE_MAX_EXPERTS)];
+  if (a >= active) return;
+  const int n = end_pair - first;
   const MxGeometry geo = mx_geometry((int64_t)p.E * 2 * p.I, p.H);
 
-  const uint8_t *wt[2], *ws[2];
-  uint32_t rowmax[2];
+  const uint8_t *wt[SP], *ws[SP];
+  uint32_t rowmax[SP];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t t = (int64_t)e * 2 * strips + i * strips + s;
+  for (int i = 0; i < SP; ++i) {
+    const int64_t t = (int64_t)e * 2 * strips + (i & 1) * strips + min(s0 + i / 2, strips - 1);
     wt[i] = p.w1 + t * geo.KT * TILE_BYTES + 16 * lane;
     ws[i] = p.w1 + geo.s_off + t * geo.KQ * 256 + 4 * lane;
     rowmax[i] = p.w1[geo.e_off + 16 * t + c];
   }
-  const uint16_t* row[QT];
-#pragma unroll
-  for (int u = 0; u < QT; ++u)
-    row[u] = p.x + (int64_t)(r->list[first + min(16 * u + c, n - 1)] / p.top) * p.H;
-  f4 acc[2][QT];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int u = 0; u < QT; ++u) acc[i][u] = f4{0.f, 0.f, 0.f, 0.f};
-
-  constexpr int U = 2;
   const int end = geo.KT * (wave + 1) / MOE_WAVES;
-  for (int kt = geo.KT * wave / MOE_WAVES; kt < end; kt += U) {
-    u4 w[U][2];
-    uint32_t sc[U][2];
+  f4* sums = reinterpret_cast<f4*>(smem);                // [wave][SP][QT][64]
+
+  for (int n0 = 0; n0 < n; n0 += 16 * QT) {
+    const uint16_t* row[QT];
 #pragma unroll
-    for (int j = 0; j < U; ++j)
+    for (int u = 0; u < QT; ++u)
+      row[u] = p.x + (int64_t)(r->list[first + min(n0 + 16 * u + c, n - 1)] / p.top) * p.H;
+    f4 acc[SP][QT];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int x = min(kt + j, end - 1);
-        w[j][i] = *reinterpret_cast<const u4*>(wt[i] + (int64_t)x * TILE_BYTES);
-        sc[j][i] = ws[i][(x >> 2) * 256 + (x & 3)];
+    for (int i = 0; i < SP; ++i)
+#pragma unroll
+      for (int u = 0; u < QT; ++u) acc[i][u] = f4{0.f, 0.f, 0.f, 0.f};
+
+    constexpr int U = P == 1 ? 2 : 1;
+    for (int kt = geo.KT * wave / MOE_WAVES; kt < end; kt += U) {
+      u4 w[U][SP];
+      uint32_t sc[U][SP];
+      h8 f[U][QT][4];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int x = min(kt + j, end - 1), k = 128 * x + 32 * g;
+#pragma unroll
+        for (int i = 0; i < SP; ++i) {
+          w[j][i] = *reinterpret_cast<const u4*>(wt[i] + (int64_t)x * TILE_BYTES);
+          sc[j][i] = ws[i][(x >> 2) * 256 + (x & 3)];
+        }
+#pragma unroll
+        for (int u = 0; u < QT; ++u)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            f[j][u][y] = *reinterpret_cast<const h8*>(k < p.H ? (const uint8_t*)(row[u] + k + 8 * y) : mx_zeros);
       }
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if (kt + j >= end) break;
-      const int k = 128 * (kt + j) + 32 * g;
-      float up[2];
+      for (int j = 0; j < U; ++j) {
+        if (kt + j >= end) break;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) up[i] = h_scale(sc[j][i], rowmax[i]);
+        for (int i = 0; i < SP; ++i) {
+          const float up = h_scale(sc[j][i], rowmax[i]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const h8 b0 = fp4_h8(w[j][0][x], up[0]), b1 = fp4_h8(w[j][1][x], up[1]);
+          for (int y = 0; y < 4; ++y) {
+            const h8 b = fp4_h8(w[j][i][y], up);
 #pragma unroll
-        for (int u = 0; u < QT; ++u) {
-          if (16 * u >= n) break;
-          const h8 f = *reinterpret_cast<const h8*>(k < p.H ? (const uint8_t*)(row[u] + k + 8 * x) : mx_zeros);
-          acc[0][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b0, f, acc[0][u], 0, 0, 0);
-          acc[1][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b1, f, acc[1][u], 0, 0, 0);
+            for (int u = 0; u < QT; ++u)
+              acc[i][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, f[j][u][y], acc[i][u], 0, 0, 0);
+          }
         }
       }
     }
-  }
 
-  f4* sums = reinterpret_cast<f4*>(smem);                // [wave][gate, up][QT][64]
+    if (n0 > 0) __syncthreads();                         // the sums before are read out
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < SP; ++i)
 #pragma unroll
-    for (int u = 0; u < QT; ++u) sums[((wave * 2 + i) * QT + u) * 64 + lane] = acc[i][u];
+      for (int u = 0; u < QT; ++u) sums[((wave * SP + i) * QT + u) * 64 + lane] = acc[i][u];
+    __syncthreads();
+    for (int x = threadIdx.x; x < P * QT * 64; x += MOE_THREADS) {
+      const int l = x & 63, u = (x >> 6) % QT, i = (x >> 6) / QT;
+      const int col = n0 + 16 * u + (l & 15), s = s0 + i;
+      if (col >= n || s >= strips) continue;
+      f4 gv = {0.f, 0.f, 0.f, 0.f}, uv = gv;
+#pragma unroll
+      for (int z = 0; z < MOE_WAVES; ++z) {
+        const f4 ga = sums[((z * SP + 2 * i) * QT + u) * 64 + l], ua = sums[((z * SP + 2 * i + 1) * QT + u) * 64 + l];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) gv[y] += ga[y], uv[y] += ua[y];
+      }
+      const uint8_t* top0 = p.w1 + geo.e_off + ((int64_t)e * 2 * strips + s) * 16 + 4 * (l >> 4);
+      const int pair = r->list[first + col];
+      const float weight = r->weight[pair];
+      b4v hi, lo;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float gate = ldexpf(gv[y], (int)top0[y] - 127 - H_UP);
+        const float h = weight * (moe_act(gate, p.act) * ldexpf(uv[y], (int)top0[16 * strips + y] - 127 - H_UP));
+        hi[y] = (__bf16)h;
+        const float rest = h - (float)hi[y];
+        lo[y] = (__bf16)(abs_bits((float)hi[y]) >= F32_INF ? 0.f : rest);
+      }
+      const int64_t at = (int64_t)pair * p.I + 16 * s + 4 * (l >> 4);
+      *reinterpret_cast<u2*>(p.h + at) = __builtin_bit_cast(u2, hi);
+      *reinterpret_cast<u2*>(p.h + (int64_t)p.T * p.top * p.I + at) = __builtin_bit_cast(u2, lo);
+    }
+  }
+}
+
+// eight weights as bfloat16 (exact: two bits of mantissa, any power of two)
+__device__ __forceinline__ b8v fp4_b8(uint32_t w, float scale) {
+  const b2v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
+  const b2v b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+  const b2v c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
+  const b2v d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+  return b8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+// a lane's 32 elements of h, hi and lo, in a k tile; zeros for pair -1 and past the end
+struct HFrag {
+  b8v hi[4], lo[4];
+};
+__device__ __forceinline__ void load_h(const MoeParams& p, int pair, int k, HFrag& f) {
+  const bool in = pair >= 0 && k < p.I;
+  const __bf16* a = p.h + (int64_t)pair * p.I + k;
+  const __bf16* b = a + (int64_t)p.T * p.top * p.I;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    f.hi[x] = *reinterpret_cast<const b8v*>(in ? (const uint8_t*)(a + 8 * x) : mx_zeros);
+    f.lo[x] = *reinterpret_cast<const b8v*>(in ? (const uint8_t*)(b + 8 * x) : mx_zeros);
+  }
+}
+__device__ __forceinline__ f4 down_product(const u4 w, uint32_t byte, const HFrag& f, f4 d) {
+  const float s = e8m0(byte);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const b8v b = fp4_b8(w[x], s);
+    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, f.hi[x], d, 0, 0, 0);
+    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, f.lo[x], d, 0, 0, 0);
+  }
+  return d;
+}
+
+// Up to 16 tokens: they are the columns, a block takes every expert in use for its
+// strip and a token's sum over them stays in its registers.
+__global__ __launch_bounds__(MOE_THREADS) void k_moe_down_tokens(const MoeParams p) {
+  __shared__ f4 sums[MOE_WAVES][64];
+  __shared__ int16_t expert[MOE_COLS * W4_MOE_MAX_TOP], column[MOE_COLS * W4_MOE_MAX_TOP][MOE_COLS];
+  const MoeRoute& r = *p.route;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int strips = p.H / 16, strip = block_number();
+  if (strip >= strips) return;
+  const int active = r.active;
+  for (int i = threadIdx.x; i < active; i += MOE_THREADS) expert[i] = (int16_t)r.expert[i];
+  for (int i = threadIdx.x; i < active * MOE_COLS / 2; i += MOE_THREADS)
+    reinterpret_cast<uint32_t*>(column)[i] = reinterpret_cast<const uint32_t*>(r.column)[i];
   __syncthreads();
-  for (int x = threadIdx.x; x < QT * 64; x += MOE_THREADS) {
-    const int l = x & 63, u = x >> 6, col = 16 * u + (l & 15), i = 16 * s + 4 * (l >> 4);
-    if (col >= n) continue;
-    f4 gv = {0.f, 0.f, 0.f, 0.f}, uv = gv;
-    for (int z = 0; z < MOE_WAVES; ++z) {
-      const f4 ga = sums[(z * 2 * QT + u) * 64 + l], ua = sums[((z * 2 + 1) * QT + u) * 64 + l];
+  const MxGeometry geo = mx_geometry((int64_t)p.E * p.H, p.I);
+  f4 acc = {0.f, 0.f, 0.f, 0.f};
+  // a unit: expert in use, k tile
+  const int units = active * geo.KT;
+  const int end = (int)((int64_t)units * (wave + 1) / MOE_WAVES);
+  int unit = (int)((int64_t)units * wave / MOE_WAVES);
+  int ex = unit / geo.KT, kt = unit - ex * geo.KT;
+  constexpr int U = 2;
+  for (; unit < end; unit += U) {
+    u4 w[U];
+    uint32_t s[U];
+    int pair[U];
+    HFrag f[U];
 #pragma unroll
-      for (int y = 0; y < 4; ++y) gv[y] += ga[y], uv[y] += ua[y];
+    for (int j = 0; j < U; ++j) {
+      const int64_t t = (int64_t)expert[ex] * strips + strip;
+      w[j] = *reinterpret_cast<const u4*>(p.w2 + (t * geo.KT + kt) * TILE_BYTES + 16 * lane);
+      s[j] = p.w2[geo.s_off + (t * geo.KQ + (kt >> 2)) * 256 + 4 * lane + (kt & 3)];
+      pair[j] = column[ex][c];
+      load_h(p, pair[j], 128 * kt + 32 * g, f[j]);
+      if (unit + j + 1 < end && ++kt == geo.KT) kt = 0, ++ex;
     }
-    const uint8_t* top0 = p.w1 + geo.e_off + ((int64_t)e * 2 * strips + s) * 16 + 4 * (l >> 4);
-    f4 h;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const float gate = ldexpf(gv[y], (int)top0[y] - 127 - H_UP);
-      h[y] = moe_act(gate, p.act) * ldexpf(uv[y], (int)top0[16 * strips + y] - 127 - H_UP);
+    for (int j = 0; j < U; ++j) {
+      if (unit + j >= end) break;
+      const f4 d = down_product(w[j], s[j], f[j], acc);
+      // a token that did not choose the expert takes nothing, NaN weights neither
+#pragma unroll
+      for (int y = 0; y < 4; ++y) acc[y] = pair[j] >= 0 ? d[y] : acc[y];
     }
-    *reinterpret_cast<f4*>(p.h + (int64_t)r->list[first + col] * p.I + i) = h;
   }
+  sums[wave][lane] = acc;
+  __syncthreads();
+  if (wave > 0 || c >= p.T) return;
+  const float nan = __uint_as_float(0x7FC00000u);
+  f4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int z = 0; z < MOE_WAVES; ++z)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) v[y] += sums[z][lane][y];
+  h4 o;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) o[y] = (_Float16)(r.bad[c] ? nan : v[y]);
+  *reinterpret_cast<u2*>(p.out + (int64_t)c * p.H + 16 * strip + 4 * g) = __builtin_bit_cast(u2, o);
 }
 
-// The largest power of two that brings values of magnitude m into fp16's range, as a
-// factor, and its reciprocal
-__device__ __forceinline__ void h_factor(float m, float& up, float& down) {
-  const int e = min(max((int)(__float_as_uint(m) >> 23), 20), 230);  // also of infinity
-  up = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
-  down = __uint_as_float((uint32_t)(e - 14) << 23);
-}
-
-// TOKENS: a block takes every expert in use for its strip, columns are the tokens
-// (up to 16), and the sums over a token's experts stay in its registers.
-// Otherwise: SP strips of one expert for its pairs, joined by the last block of a
-// strip group.
-template <int QT, int SP, bool TOKENS>
-__global__ __launch_bounds__(MOE_THREADS) void k_moe_down(const MoeParams p) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+// SP strips of one expert for its pairs, 16 of them at a time; the last block of a
+// group of strips sums each token's pairs, in the order of its choices.
+template <int SP>
+__global__ __launch_bounds__(MOE_THREADS) void k_moe_down_pairs(const MoeParams p) {
+  __shared__ f4 sums[MOE_WAVES][SP][64];
   __shared__ unsigned slast;
-  static_assert(!TOKENS || QT == 1, "tokens are the columns of one operand");
   const MoeRoute& r = *p.route;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int strips = p.H / 16, groups = (strips + SP - 1) / SP;
-  const int a = TOKENS ? 0 : block_number() / groups;
-  const int grp = block_number() - a * groups;
-  if (grp >= groups || (!TOKENS && a > 0 && a >= r.active)) return;
-  const bool empty = !TOKENS && r.active == 0;           // no token chose: the rows are 0
-  const int experts = TOKENS ? r.active : empty ? 0 : 1;
-  const int first = TOKENS || empty ? 0 : r.first[a], n = TOKENS ? p.T : empty ? 0 : r.first[a + 1] - first;
-  const MxGeometry geo = mx_geometry((int64_t)p.E * p.H, p.I);
-
-  f4 acc[SP][QT];
-#pragma unroll
-  for (int i = 0; i < SP; ++i)
-#pragma unroll
-    for (int u = 0; u < QT; ++u) acc[i][u] = f4{0.f, 0.f, 0.f, 0.f};
-
-  const int units = experts * geo.KT;
-  const int end = (int)((int64_t)units * (wave + 1) / MOE_WAVES);
-  int unit = (int)((int64_t)units * wave / MOE_WAVES);
-  int ex = unit / geo.KT, kt = unit - ex * geo.KT;       // a unit: expert, k tile
-  int pair[QT];
-  auto enter = [&] {                                     // this lane's pairs of expert ex, -1 for none
-    if constexpr (TOKENS) {
-      pair[0] = -1;
-      const int f = r.first[ex], l = r.first[ex + 1];
-      for (int i = f; i < l; ++i)
-        if (r.list[i] / p.top == c) pair[0] = r.list[i];
-    } else {
-#pragma unroll
-      for (int u = 0; u < QT; ++u) pair[u] = 16 * u + c < n ? r.list[first + 16 * u + c] : -1;
-    }
-  };
-  if (unit < end) enter();
-  for (; unit < end; ++unit) {
-    const int64_t t = (int64_t)r.expert[a + ex] * strips + grp * SP;
-    u4 w[SP];
-    float up[SP];
-#pragma unroll
-    for (int i = 0; i < SP; ++i) {
-      const int64_t ti = t + min(i, strips - 1 - grp * SP);
-      w[i] = *reinterpret_cast<const u4*>(p.w2 + (ti * geo.KT + kt) * TILE_BYTES + 16 * lane);
-      const uint32_t byte = p.w2[geo.s_off + (ti * geo.KQ + (kt >> 2)) * 256 + 4 * lane + (kt & 3)];
-      up[i] = h_scale(byte, p.w2[geo.e_off + 16 * ti + c]);
-    }
-    h8 hf[QT][4];
-    float down[QT];
-    const int k = 128 * kt + 32 * g;
-#pragma unroll
-    for (int u = 0; u < QT; ++u) {
-      float v[32];
-      const bool in = pair[u] >= 0 && k < p.I;
-      const float* hp = p.h + (int64_t)max(pair[u], 0) * p.I + min(k, p.I - 32);
-      const float weight = TOKENS && in ? r.weight[pair[u]] : 1.f;
-      float m = 0.f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const f4 x = *reinterpret_cast<const f4*>(hp + 4 * q);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          v[4 * q + y] = in ? x[y] * weight : 0.f;
-          m = fmaxf(m, fabsf(v[4 * q + y]));
-        }
-      }
-      m = fmaxf(m, __shfl_xor(m, 16, 64));
-      m = fmaxf(m, __shfl_xor(m, 32, 64));
-      float f;
-      h_factor(m, f, down[u]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int y = 0; y < 8; ++y) hf[u][q][y] = (_Float16)(v[8 * q + y] * f);
-    }
-#pragma unroll
-    for (int i = 0; i < SP; ++i) {
-      f4 d[QT];
-#pragma unroll
-      for (int u = 0; u < QT; ++u) d[u] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const h8 b = fp4_h8(w[i][x], up[i]);
-#pragma unroll
-        for (int u = 0; u < QT; ++u) d[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, hf[u][x], d[u], 0, 0, 0);
-      }
-      // rows 4 g .. of the strip, each counted from its largest scale
-      const int64_t ti = t + min(i, strips - 1 - grp * SP);
-      const uint32_t tops = *reinterpret_cast<const uint32_t*>(p.w2 + geo.e_off + 16 * ti + 4 * g);
-#pragma unroll
-      for (int u = 0; u < QT; ++u)
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          // a token that did not choose the expert takes nothing, NaN weights neither
-          if (!TOKENS || pair[u] >= 0)
-            acc[i][u][y] += ldexpf(d[u][y] * down[u], (int)(tops >> (8 * y) & 255u) - 127 - H_UP);
-    }
-    if (++kt == geo.KT) {
-      kt = 0;
-      ++ex;
-      if (unit + 1 < end) enter();
-    }
-  }
-
-  f4* sums = reinterpret_cast<f4*>(smem);                // [wave][SP][QT][64]
-#pragma unroll
-  for (int i = 0; i < SP; ++i)
-#pragma unroll
-    for (int u = 0; u < QT; ++u) sums[((wave * SP + i) * QT + u) * 64 + lane] = acc[i][u];
-  __syncthreads();
-  const float nan = __uint_as_float(0x7FC00000u);
-  for (int x = threadIdx.x; x < SP * QT * 64; x += MOE_THREADS) {
-    const int l = x & 63, u = (x >> 6) % QT, i = (x >> 6) / QT;
-    const int col = 16 * u + (l & 15), strip = grp * SP + i;
-    if (col >= n || strip >= strips) continue;
-    f4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int z = 0; z < MOE_WAVES; ++z) {
-      const f4 q = sums[((z * SP + i) * QT + u) * 64 + l];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) v[y] += q[y];
-    }
-    const int at = 16 * strip + 4 * (l >> 4);
-    if constexpr (TOKENS) {
-      h4 o;
-#pragma unroll
-      for (int y = 0; y < 4; ++y) o[y] = (_Float16)(r.bad[col] ? nan : v[y]);
-      *reinterpret_cast<u2*>(p.out + (int64_t)col * p.H + at) = __builtin_bit_cast(u2, o);
-    } else {
-      const int pr = r.list[first + col];
-      const float wgt = r.weight[pr];
-      uint32_t* y = reinterpret_cast<uint32_t*>(p.y) + (int64_t)pr * p.H + at;
-      dev_store2(y, __float_as_uint(v[0] * wgt), __float_as_uint(v[1] * wgt));
-      dev_store2(y + 2, __float_as_uint(v[2] * wgt), __float_as_uint(v[3] * wgt));
-    }
-  }
-  if constexpr (TOKENS) return;
+  const int a = block_number() / groups, grp = block_number() - a * groups;
+  const int active = r.active;
+  if (a > 0 && a >= active) return;
+  const bool empty = active == 0;                        // no token chose: the rows are 0
   if (!empty) {
+    const int first = r.first[a], n = r.first[a + 1] - first;
+    const MxGeometry geo = mx_geometry((int64_t)p.E * p.H, p.I);
+    const int64_t t = (int64_t)r.expert[a] * strips + grp * SP;
+    const uint8_t *wt[SP], *ws[SP];
+#pragma unroll
+    for (int i = 0; i < SP; ++i) {
+      const int64_t ti = t + min(i, strips - 1 - grp * SP);
+      wt[i] = p.w2 + ti * geo.KT * TILE_BYTES + 16 * lane;
+      ws[i] = p.w2 + geo.s_off + ti * geo.KQ * 256 + 4 * lane;
+    }
+    const int end = geo.KT * (wave + 1) / MOE_WAVES;
+    for (int n0 = 0; n0 < n; n0 += 16) {
+      const int pair = n0 + c < n ? r.list[first + n0 + c] : -1;
+      f4 acc[SP];
+#pragma unroll
+      for (int i = 0; i < SP; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
+      for (int kt = geo.KT * wave / MOE_WAVES; kt < end; ++kt) {
+        u4 w[SP];
+        uint32_t s[SP];
+        HFrag f;
+#pragma unroll
+        for (int i = 0; i < SP; ++i) {
+          w[i] = *reinterpret_cast<const u4*>(wt[i] + (int64_t)kt * TILE_BYTES);
+          s[i] = ws[i][(kt >> 2) * 256 + (kt & 3)];
+        }
+        load_h(p, pair, 128 * kt + 32 * g, f);
+#pragma unroll
+        for (int i = 0; i < SP; ++i) acc[i] = down_product(w[i], s[i], f, acc[i]);
+      }
+      if (n0 > 0) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < SP; ++i) sums[wave][i][lane] = acc[i];
+      __syncthreads();
+      for (int x = threadIdx.x; x < SP * 64; x += MOE_THREADS) {
+        const int l = x & 63, i = x >> 6, col = n0 + (l & 15), strip = grp * SP + i;
+        if (col >= n || strip >= strips) continue;
+        f4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int z = 0; z < MOE_WAVES; ++z)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) v[y] += sums[z][i][l][y];
+        uint32_t* y = reinterpret_cast<uint32_t*>(p.y) + (int64_t)r.list[first + col] * p.H + 16 * strip + 4 * (l >> 4);
+        dev_store2(y, __float_as_uint(v[0]), __float_as_uint(v[1]));
+        dev_store2(y + 2, __float_as_uint(v[2]), __float_as_uint(v[3]));
+      }
+    }
     stores_done();
     __syncthreads();
-    if (threadIdx.x == 0) slast = dev_arrive(p.counters + grp) == (unsigned)(r.active - 1);
+    if (threadIdx.x == 0) slast = dev_arrive(p.counters + grp) == (unsigned)(active - 1);
     __syncthreads();
     if (!slast) return;
     if (threadIdx.x == 0) dev_store(p.counters + grp, 0u);
   }
-  // the last block of these columns: each token's pairs in the order of its choices
+  const float nan = __uint_as_float(0x7FC00000u);
   for (int x = threadIdx.x; x < p.T * SP * 4; x += MOE_THREADS) {
     const int tok = x / (SP * 4), col = 16 * SP * grp + 4 * (x % (SP * 4));
     if (col >= p.H) continue;
     f4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < p.top; ++j) {
-      const int pr = tok * p.top + j;
-      if (empty || r.weight[pr] < 0.f) continue;
-      const uint32_t* y = reinterpret_cast<const uint32_t*>(p.y) + (int64_t)pr * p.H + col;
-      const uint64_t lo = dev_load2(y), hi = dev_load2(y + 2);
-      v[0] += __uint_as_float((uint32_t)lo), v[1] += __uint_as_float((uint32_t)(lo >> 32));
-      v[2] += __uint_as_float((uint32_t)hi), v[3] += __uint_as_float((uint32_t)(hi >> 32));
+    if (!empty) {
+      uint64_t lo[W4_MOE_MAX_TOP], hi[W4_MOE_MAX_TOP];
+      float weight[W4_MOE_MAX_TOP];
+#pragma unroll
+      for (int j = 0; j < W4_MOE_MAX_TOP; ++j)
+        if (j < p.top) {
+          const int pr = tok * p.top + j;
+          const uint32_t* y = reinterpret_cast<const uint32_t*>(p.y) + (int64_t)pr * p.H + col;
+          weight[j] = r.weight[pr];
+          lo[j] = dev_load2(y), hi[j] = dev_load2(y + 2);
+        }
+#pragma unroll
+      for (int j = 0; j < W4_MOE_MAX_TOP; ++j)
+        if (j < p.top && weight[j] >= 0.f) {
+          v[0] += __uint_as_float((uint32_t)lo[j]), v[1] += __uint_as_float((uint32_t)(lo[j] >> 32));
+          v[2] += __uint_as_float((uint32_t)hi[j]), v[3] += __uint_as_float((uint32_t)(hi[j] >> 32));
+        }
     }
     h4 o;
 #pragma unroll
@@ -440,7 +505,8 @@ static bool moe_sizes_ok(int T, int H, int I, int E, int top) {
          top <= W4_MOE_MAX_TOP && top <= E && H >= 32 && H % 32 == 0 && H <= W4_MAX_K && I >= 32 &&
          I % 32 == 0 && I <= W4_MAX_K;
 }
-static bool moe_tokens(int T) { return T <= 16; }        // tokens as columns, nothing to join
+// tokens as columns, nothing to join: where a strip a block gives the CUs work
+static bool moe_columns(int T, int H) { return T <= MOE_COLS && H >= 128 * 16; }
 
 struct MoeSpace {
   int64_t h, y, total;
@@ -449,27 +515,27 @@ static MoeSpace moe_space(int T, int H, int I, int top) {
   MoeSpace s;
   s.h = WS_COUNTERS + (int64_t)((sizeof(MoeRoute) + 255) / 256 * 256);
   s.y = s.h + (int64_t)T * top * I * 4;
-  s.total = s.y + (moe_tokens(T) ? 0 : (int64_t)T * top * H * 4);
+  s.total = s.y + (moe_columns(T, H) ? 0 : (int64_t)T * top * H * 4);
   return s;
 }
 
-template <int QT>
-int launch_up(const MoeParams& p, bool route, int64_t blocks, hipStream_t stream) {
-  constexpr int lds = MOE_WAVES * 2 * QT * 1024;
-  if (route) {
-    if constexpr (QT == 1)
-      hipLaunchKernelGGL((k_moe_up<1, true>), grid_of(blocks), dim3(MOE_THREADS), lds, stream, p);
-  } else {
-    hipLaunchKernelGGL((k_moe_up<QT, false>), grid_of(blocks), dim3(MOE_THREADS), lds, stream, p);
-  }
+template <int P, int QT, int R>
+int launch_up_r(const MoeParams& p, int64_t experts, hipStream_t stream) {
+  constexpr int lds = MOE_WAVES * 2 * P * QT * 1024;
+  allow_smem((const void*)&k_moe_up<P, QT, R>, lds);
+  hipLaunchKernelGGL((k_moe_up<P, QT, R>), grid_of(experts * ((p.I / 16 + P - 1) / P)), dim3(MOE_THREADS),
+                     lds, stream, p);
   return launch_status();
 }
-template <int QT>
-int launch_down(const MoeParams& p, int64_t blocks, hipStream_t stream) {
-  constexpr int lds = MOE_WAVES * DOWN_SP * QT * 1024;
-  allow_smem((const void*)&k_moe_down<QT, DOWN_SP, false>, lds);
-  hipLaunchKernelGGL((k_moe_down<QT, DOWN_SP, false>), grid_of(blocks), dim3(MOE_THREADS), lds, stream, p);
-  return launch_status();
+template <int P>
+int launch_up(const MoeParams& p, bool in, int64_t experts, hipStream_t stream) {
+  if (in)
+    return p.E <= 64    ? launch_up_r<P, 1, 1>(p, experts, stream)
+           : p.E <= 128 ? launch_up_r<P, 1, 2>(p, experts, stream)
+                        : launch_up_r<P, 1, 8>(p, experts, stream);
+  // two column operands where an expert has more than 12 pairs in the mean
+  return p.T * p.top > 12 * p.E ? launch_up_r<P, 2, 0>(p, experts, stream)
+                                : launch_up_r<P, 1, 0>(p, experts, stream);
 }
 
 }  // namespace w4
@@ -499,26 +565,24 @@ extern "C" int moe_mx4(const uint16_t* x, const void* logits, int logits_dtype, 
   MoeParams p{};
   p.x = x, p.logits = logits, p.w1 = w_gate_up, p.w2 = w_down, p.out = out;
   p.counters = (uint32_t*)ws, p.route = (MoeRoute*)(ws + WS_COUNTERS);
-  p.h = (float*)(ws + s.h), p.y = (float*)(ws + s.y);
+  p.h = (__bf16*)(ws + s.h), p.y = (float*)(ws + s.y);
   p.T = tokens, p.H = hidden, p.I = inner, p.E = experts, p.top = top_k, p.act = act;
   p.renorm = renormalize != 0, p.half_logits = logits_dtype == W4_IN_F16;
 
-  const bool route = tokens <= ROUTE_IN;
-  if (!route) {
-    hipLaunchKernelGGL(k_moe_route, dim3(1), dim3(MOE_THREADS), 0, stream, p);
+  const bool in = tokens <= ROUTE_IN;
+  if (!in) {
+    if (experts <= 64) hipLaunchKernelGGL(k_moe_route<1>, dim3(1), dim3(ROUTE_THREADS), 0, stream, p);
+    else if (experts <= 128) hipLaunchKernelGGL(k_moe_route<2>, dim3(1), dim3(ROUTE_THREADS), 0, stream, p);
+    else hipLaunchKernelGGL(k_moe_route<8>, dim3(1), dim3(ROUTE_THREADS), 0, stream, p);
     if (const int st = launch_status()) return st;
   }
   const int64_t most = min(experts, tokens * top_k);     // experts in use, at most
-  const int64_t up = most * (inner / 16);
-  const int st = tokens <= 16   ? launch_up<1>(p, route, up, stream)
-                 : tokens <= 32 ? launch_up<2>(p, route, up, stream)
-                                : launch_up<4>(p, route, up, stream);
+  const int st = most * (inner / 16) > 1024 ? launch_up<2>(p, in, most, stream) : launch_up<1>(p, in, most, stream);
   if (st) return st;
-  if (moe_tokens(tokens)) {
-    hipLaunchKernelGGL((k_moe_down<1, 1, true>), grid_of(hidden / 16), dim3(MOE_THREADS),
-                       MOE_WAVES * 1024, stream, p);
-    return launch_status();
-  }
-  const int64_t down = most * ((hidden / 16 + DOWN_SP - 1) / DOWN_SP);
-  return tokens <= 32 ? launch_down<2>(p, down, stream) : launch_down<4>(p, down, stream);
+  if (moe_columns(tokens, hidden))
+    hipLaunchKernelGGL(k_moe_down_tokens, grid_of(hidden / 16), dim3(MOE_THREADS), 0, stream, p);
+  else
+    hipLaunchKernelGGL(k_moe_down_pairs<DOWN_SP>, grid_of(most * ((hidden / 16 + DOWN_SP - 1) / DOWN_SP)),
+                       dim3(MOE_THREADS), 0, stream, p);
+  return launch_status();
 }
