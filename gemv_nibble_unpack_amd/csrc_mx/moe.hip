@@ -207,10 +207,11 @@ __global__ __launch_bounds__(MOE_THREADS) void k_moe_up(const MoeParams p) {
     r = &own;
   }
   const int active = r->active;
-  const int e = r->expert[min(a, W4_MOE_MAX_EXPERTS - 1)], first = r->first[min(a, W4_MOE_MAX_EXPERTS - 1)];
-  const int end_pair = r->first[min(a + 1, W4_MOE_MAX_EXPERTS)];
+  // (the weights' addresses in scalar registers)
+  const int e = __builtin_amdgcn_readfirstlane(r->expert[min(a, W4_MOE_MAX_EXPERTS - 1)]);
+  const int first = __builtin_amdgcn_readfirstlane(r->first[min(a, W4_MOE_MAX_EXPERTS - 1)]);
+  const int n = __builtin_amdgcn_readfirstlane(r->first[min(a + 1, W4_MOE_MAX_EXPERTS)]) - first;
   if (a >= active) return;
-  const int n = end_pair - first;
   const MxGeometry geo = mx_geometry((int64_t)p.E * 2 * p.I, p.H);
 
   const uint8_t *wt[SP], *ws[SP];
@@ -218,8 +219,8 @@ __global__ __launch_bounds__(MOE_THREADS) void k_moe_up(const MoeParams p) {
 #pragma unroll
   for (int i = 0; i < SP; ++i) {
     const int64_t t = (int64_t)e * 2 * strips + (i & 1) * strips + min(s0 + i / 2, strips - 1);
-    wt[i] = p.w1 + t * geo.KT * TILE_BYTES + 16 * lane;
-    ws[i] = p.w1 + geo.s_off + t * geo.KQ * 256 + 4 * lane;
+    wt[i] = p.w1 + t * geo.KT * TILE_BYTES;
+    ws[i] = p.w1 + geo.s_off + t * geo.KQ * 256;
     rowmax[i] = p.w1[geo.e_off + 16 * t + c];
   }
   const int end = geo.KT * (wave + 1) / MOE_WAVES;
@@ -246,14 +247,14 @@ __global__ __launch_bounds__(MOE_THREADS) void k_moe_up(const MoeParams p) {
         const int x = min(kt + j, end - 1), k = 128 * x + 32 * g;
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
-          w[j][i] = *reinterpret_cast<const u4*>(wt[i] + (int64_t)x * TILE_BYTES);
-          sc[j][i] = ws[i][(x >> 2) * 256 + (x & 3)];
+          w[j][i] = g_load<u4>(wt[i] + (int64_t)x * TILE_BYTES, 16 * lane);
+          sc[j][i] = g_load<uint8_t>(ws[i] + (x >> 2) * 256 + (x & 3), 4 * lane);
         }
 #pragma unroll
         for (int u = 0; u < QT; ++u)
 #pragma unroll
           for (int y = 0; y < 4; ++y)
-            f[j][u][y] = *reinterpret_cast<const h8*>(k < p.H ? (const uint8_t*)(row[u] + k + 8 * y) : mx_zeros);
+            f[j][u][y] = g_load<h8>(k < p.H ? (const uint8_t*)(row[u] + k + 8 * y) : mx_zeros);
       }
 #pragma unroll
       for (int j = 0; j < U; ++j) {
@@ -316,20 +317,10 @@ __device__ __forceinline__ b8v fp4_b8(uint32_t w, float scale) {
   const b2v d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
   return b8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-// a lane's 32 elements of h, hi and lo, in a k tile; zeros for pair -1 and past the end
+// a lane's 32 elements of h, hi and lo, in a k tile
 struct HFrag {
   b8v hi[4], lo[4];
 };
-__device__ __forceinline__ void load_h(const MoeParams& p, int pair, int k, HFrag& f) {
-  const bool in = pair >= 0 && k < p.I;
-  const __bf16* a = p.h + (int64_t)pair * p.I + k;
-  const __bf16* b = a + (int64_t)p.T * p.top * p.I;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    f.hi[x] = *reinterpret_cast<const b8v*>(in ? (const uint8_t*)(a + 8 * x) : mx_zeros);
-    f.lo[x] = *reinterpret_cast<const b8v*>(in ? (const uint8_t*)(b + 8 * x) : mx_zeros);
-  }
-}
 __device__ __forceinline__ f4 down_product(const u4 w, uint32_t byte, const HFrag& f, f4 d) {
   const float s = e8m0(byte);
 #pragma unroll
@@ -341,9 +332,10 @@ __device__ __forceinline__ f4 down_product(const u4 w, uint32_t byte, const HFra
   return d;
 }
 
-// Up to 16 tokens: they are the columns, a block takes every expert in use for its
-// strip and a token's sum over them stays in its registers.
+// A few tokens whose h fits in LDS: the tokens are the columns, a block takes every
+// expert in use for its strip and a token's sum over them stays in its registers.
 __global__ __launch_bounds__(MOE_THREADS) void k_moe_down_tokens(const MoeParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];     // h, then 16 bytes of zeros
   __shared__ f4 sums[MOE_WAVES][64];
   __shared__ int16_t expert[MOE_COLS * W4_MOE_MAX_TOP], column[MOE_COLS * W4_MOE_MAX_TOP][MOE_COLS];
   const MoeRoute& r = *p.route;
@@ -351,6 +343,10 @@ __global__ __launch_bounds__(MOE_THREADS) void k_moe_down_tokens(const MoeParams
   const int c = lane & 15, g = lane >> 4;
   const int strips = p.H / 16, strip = block_number();
   if (strip >= strips) return;
+  const int plane = p.T * p.top * p.I * 2;               // bytes
+  for (int i = threadIdx.x; i < plane / 8; i += MOE_THREADS)
+    reinterpret_cast<u4*>(smem)[i] = reinterpret_cast<const u4*>(p.h)[i];
+  if (threadIdx.x == 0) *reinterpret_cast<u4*>(smem + 2 * plane) = u4{0u, 0u, 0u, 0u};
   const int active = r.active;
   for (int i = threadIdx.x; i < active; i += MOE_THREADS) expert[i] = (int16_t)r.expert[i];
   for (int i = threadIdx.x; i < active * MOE_COLS / 2; i += MOE_THREADS)
@@ -362,29 +358,35 @@ __global__ __launch_bounds__(MOE_THREADS) void k_moe_down_tokens(const MoeParams
   const int units = active * geo.KT;
   const int end = (int)((int64_t)units * (wave + 1) / MOE_WAVES);
   int unit = (int)((int64_t)units * wave / MOE_WAVES);
-  int ex = unit / geo.KT, kt = unit - ex * geo.KT;
-  constexpr int U = 2;
+  constexpr int U = 8;
   for (; unit < end; unit += U) {
     u4 w[U];
     uint32_t s[U];
-    int pair[U];
-    HFrag f[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int64_t t = (int64_t)expert[ex] * strips + strip;
-      w[j] = *reinterpret_cast<const u4*>(p.w2 + (t * geo.KT + kt) * TILE_BYTES + 16 * lane);
-      s[j] = p.w2[geo.s_off + (t * geo.KQ + (kt >> 2)) * 256 + 4 * lane + (kt & 3)];
-      pair[j] = column[ex][c];
-      load_h(p, pair[j], 128 * kt + 32 * g, f[j]);
-      if (unit + j + 1 < end && ++kt == geo.KT) kt = 0, ++ex;
+      if (unit + j >= end) break;
+      const int ex = (unit + j) / geo.KT, kt = unit + j - ex * geo.KT;
+      const int64_t t = (int64_t)__builtin_amdgcn_readfirstlane(expert[ex]) * strips + strip;
+      w[j] = g_load<u4>(p.w2 + (t * geo.KT + kt) * TILE_BYTES, 16 * lane);
+      s[j] = g_load<uint8_t>(p.w2 + geo.s_off + (t * geo.KQ + (kt >> 2)) * 256 + (kt & 3), 4 * lane);
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (unit + j >= end) break;
-      const f4 d = down_product(w[j], s[j], f[j], acc);
+      const int ex = (unit + j) / geo.KT, k = 128 * (unit + j - ex * geo.KT) + 32 * g;
+      const int pair = column[ex][c];
+      const bool in = pair >= 0 && k < p.I;
+      const int at = (pair * p.I + k) * 2;
+      HFrag f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        f.hi[x] = *reinterpret_cast<const b8v*>(smem + (in ? at + 16 * x : 2 * plane));
+        f.lo[x] = *reinterpret_cast<const b8v*>(smem + (in ? at + plane + 16 * x : 2 * plane));
+      }
+      const f4 d = down_product(w[j], s[j], f, acc);
       // a token that did not choose the expert takes nothing, NaN weights neither
 #pragma unroll
-      for (int y = 0; y < 4; ++y) acc[y] = pair[j] >= 0 ? d[y] : acc[y];
+      for (int y = 0; y < 4; ++y) acc[y] = pair >= 0 ? d[y] : acc[y];
     }
   }
   sums[wave][lane] = acc;
@@ -404,8 +406,10 @@ __global__ __launch_bounds__(MOE_THREADS) void k_moe_down_tokens(const MoeParams
 
 // SP strips of one expert for its pairs, 16 of them at a time; the last block of a
 // group of strips sums each token's pairs, in the order of its choices.
+// Two blocks a CU (128 registers), a k tile's weights on their way while the one
+// before is multiplied.
 template <int SP>
-__global__ __launch_bounds__(MOE_THREADS) void k_moe_down_pairs(const MoeParams p) {
+__global__ __launch_bounds__(MOE_THREADS, 4) void k_moe_down_pairs(const MoeParams p) {
   __shared__ f4 sums[MOE_WAVES][SP][64];
   __shared__ unsigned slast;
   const MoeRoute& r = *p.route;
@@ -417,34 +421,52 @@ __global__ __launch_bounds__(MOE_THREADS) void k_moe_down_pairs(const MoeParams 
   if (a > 0 && a >= active) return;
   const bool empty = active == 0;                        // no token chose: the rows are 0
   if (!empty) {
-    const int first = r.first[a], n = r.first[a + 1] - first;
+    const int first = __builtin_amdgcn_readfirstlane(r.first[a]);
+    const int n = __builtin_amdgcn_readfirstlane(r.first[a + 1]) - first;
     const MxGeometry geo = mx_geometry((int64_t)p.E * p.H, p.I);
-    const int64_t t = (int64_t)r.expert[a] * strips + grp * SP;
+    const int64_t t = (int64_t)__builtin_amdgcn_readfirstlane(r.expert[a]) * strips + grp * SP;
     const uint8_t *wt[SP], *ws[SP];
 #pragma unroll
     for (int i = 0; i < SP; ++i) {
       const int64_t ti = t + min(i, strips - 1 - grp * SP);
-      wt[i] = p.w2 + ti * geo.KT * TILE_BYTES + 16 * lane;
-      ws[i] = p.w2 + geo.s_off + ti * geo.KQ * 256 + 4 * lane;
+      wt[i] = p.w2 + ti * geo.KT * TILE_BYTES;
+      ws[i] = p.w2 + geo.s_off + ti * geo.KQ * 256;
     }
     const int end = geo.KT * (wave + 1) / MOE_WAVES;
+    const int64_t plane = (int64_t)p.T * p.top * p.I;
     for (int n0 = 0; n0 < n; n0 += 16) {
       const int pair = n0 + c < n ? r.list[first + n0 + c] : -1;
       f4 acc[SP];
 #pragma unroll
       for (int i = 0; i < SP; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
-      for (int kt = geo.KT * wave / MOE_WAVES; kt < end; ++kt) {
-        u4 w[SP];
-        uint32_t s[SP];
-        HFrag f;
+      u4 w[SP];
+      uint32_t s[SP];
+      auto weights = [&](int kt) {
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
-          w[i] = *reinterpret_cast<const u4*>(wt[i] + (int64_t)kt * TILE_BYTES);
-          s[i] = ws[i][(kt >> 2) * 256 + (kt & 3)];
+          w[i] = g_load<u4>(wt[i] + (int64_t)kt * TILE_BYTES, 16 * lane);
+          s[i] = g_load<uint8_t>(ws[i] + (kt >> 2) * 256 + (kt & 3), 4 * lane);
         }
-        load_h(p, pair, 128 * kt + 32 * g, f);
+      };
+      int kt = geo.KT * wave / MOE_WAVES;
+      if (kt < end) weights(kt);
+      for (; kt < end; ++kt) {
+        HFrag f;
+        const int k = 128 * kt + 32 * g;
+        const bool in = pair >= 0 && k < p.I;
+        const __bf16* hp = p.h + (int64_t)pair * p.I + k;
 #pragma unroll
-        for (int i = 0; i < SP; ++i) acc[i] = down_product(w[i], s[i], f, acc[i]);
+        for (int x = 0; x < 4; ++x) {
+          f.hi[x] = g_load<b8v>(in ? (const uint8_t*)(hp + 8 * x) : mx_zeros);
+          f.lo[x] = g_load<b8v>(in ? (const uint8_t*)(hp + plane + 8 * x) : mx_zeros);
+        }
+        u4 v[SP];
+        uint32_t sv[SP];
+#pragma unroll
+        for (int i = 0; i < SP; ++i) v[i] = w[i], sv[i] = s[i];
+        if (kt + 1 < end) weights(kt + 1);
+#pragma unroll
+        for (int i = 0; i < SP; ++i) acc[i] = down_product(v[i], sv[i], f, acc[i]);
       }
       if (n0 > 0) __syncthreads();
 #pragma unroll
@@ -476,22 +498,24 @@ __global__ __launch_bounds__(MOE_THREADS) void k_moe_down_pairs(const MoeParams 
     if (col >= p.H) continue;
     f4 v = {0.f, 0.f, 0.f, 0.f};
     if (!empty) {
-      uint64_t lo[W4_MOE_MAX_TOP], hi[W4_MOE_MAX_TOP];
-      float weight[W4_MOE_MAX_TOP];
+      // four choices' loads together: each is a round trip to the level that all XCDs share
+      for (int j0 = 0; j0 < p.top; j0 += 4) {
+        uint64_t lo[4], hi[4];
+        float weight[4];
 #pragma unroll
-      for (int j = 0; j < W4_MOE_MAX_TOP; ++j)
-        if (j < p.top) {
-          const int pr = tok * p.top + j;
+        for (int j = 0; j < 4; ++j) {
+          const int pr = tok * p.top + min(j0 + j, p.top - 1);
           const uint32_t* y = reinterpret_cast<const uint32_t*>(p.y) + (int64_t)pr * p.H + col;
           weight[j] = r.weight[pr];
           lo[j] = dev_load2(y), hi[j] = dev_load2(y + 2);
         }
 #pragma unroll
-      for (int j = 0; j < W4_MOE_MAX_TOP; ++j)
-        if (j < p.top && weight[j] >= 0.f) {
-          v[0] += __uint_as_float((uint32_t)lo[j]), v[1] += __uint_as_float((uint32_t)(lo[j] >> 32));
-          v[2] += __uint_as_float((uint32_t)hi[j]), v[3] += __uint_as_float((uint32_t)(hi[j] >> 32));
-        }
+        for (int j = 0; j < 4; ++j)
+          if (j0 + j < p.top && weight[j] >= 0.f) {
+            v[0] += __uint_as_float((uint32_t)lo[j]), v[1] += __uint_as_float((uint32_t)(lo[j] >> 32));
+            v[2] += __uint_as_float((uint32_t)hi[j]), v[3] += __uint_as_float((uint32_t)(hi[j] >> 32));
+          }
+      }
     }
     h4 o;
 #pragma unroll
@@ -505,8 +529,12 @@ static bool moe_sizes_ok(int T, int H, int I, int E, int top) {
          top <= W4_MOE_MAX_TOP && top <= E && H >= 32 && H % 32 == 0 && H <= W4_MAX_K && I >= 32 &&
          I % 32 == 0 && I <= W4_MAX_K;
 }
-// tokens as columns, nothing to join: where a strip a block gives the CUs work
-static bool moe_columns(int T, int H) { return T <= MOE_COLS && H >= 128 * 16; }
+// tokens as columns, nothing to join: where a strip a block gives the CUs work and h
+// (4 bytes an element) fits in LDS
+constexpr int MOE_H_LDS = 64 * 1024;
+static bool moe_columns(int T, int H, int I, int top) {
+  return T <= MOE_COLS && H >= 128 * 16 && (int64_t)T * top * I * 4 <= MOE_H_LDS;
+}
 
 struct MoeSpace {
   int64_t h, y, total;
@@ -515,7 +543,7 @@ static MoeSpace moe_space(int T, int H, int I, int top) {
   MoeSpace s;
   s.h = WS_COUNTERS + (int64_t)((sizeof(MoeRoute) + 255) / 256 * 256);
   s.y = s.h + (int64_t)T * top * I * 4;
-  s.total = s.y + (moe_columns(T, H) ? 0 : (int64_t)T * top * H * 4);
+  s.total = s.y + (moe_columns(T, H, I, top) ? 0 : (int64_t)T * top * H * 4);
   return s;
 }
 
@@ -579,9 +607,11 @@ extern "C" int moe_mx4(const uint16_t* x, const void* logits, int logits_dtype, 
   const int64_t most = min(experts, tokens * top_k);     // experts in use, at most
   const int st = most * (inner / 16) > 1024 ? launch_up<2>(p, in, most, stream) : launch_up<1>(p, in, most, stream);
   if (st) return st;
-  if (moe_columns(tokens, hidden))
-    hipLaunchKernelGGL(k_moe_down_tokens, grid_of(hidden / 16), dim3(MOE_THREADS), 0, stream, p);
-  else
+  if (moe_columns(tokens, hidden, inner, top_k)) {
+    const int lds = tokens * top_k * inner * 4 + 16;
+    allow_smem((const void*)&k_moe_down_tokens, MOE_H_LDS + 16);
+    hipLaunchKernelGGL(k_moe_down_tokens, grid_of(hidden / 16), dim3(MOE_THREADS), lds, stream, p);
+  } else
     hipLaunchKernelGGL(k_moe_down_pairs<DOWN_SP>, grid_of(most * ((hidden / 16 + DOWN_SP - 1) / DOWN_SP)),
                        dim3(MOE_THREADS), 0, stream, p);
   return launch_status();

@@ -33,6 +33,19 @@ __host__ __device__ inline MxGeometry mx_geometry(int64_t N, int K) {
   return g;
 }
 
+// Loads from global memory, said to the compiler: of a pointer chosen between a
+// tensor and a constant it makes flat loads, which also pass through the LDS side.
+#define W4_GLOBAL __attribute__((address_space(1)))
+template <typename T>
+__device__ __forceinline__ T g_load(const void* p) {
+  return *(const W4_GLOBAL T*)p;
+}
+// base the same for the wave: a scalar base and 32 bits a lane
+template <typename T>
+__device__ __forceinline__ T g_load(const void* base, uint32_t offset) {
+  return *(const W4_GLOBAL T*)((const W4_GLOBAL uint8_t*)base + offset);
+}
+
 // 2^(byte - 127), NaN for 255; byte 0 is the subnormal 2^-127
 __device__ __forceinline__ float e8m0(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);

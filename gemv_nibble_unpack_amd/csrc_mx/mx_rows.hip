@@ -35,8 +35,8 @@ __global__ __launch_bounds__(64 * ROW_WAVES) void k_mx_rows(const MxParams p) {
 #pragma unroll
   for (int i = 0; i < SP; ++i) {
     const int64_t t = min(t0 + i, geo.NT - 1);
-    wt[i] = p.Wp + t * geo.KT * TILE_BYTES + 16 * lane;
-    ws[i] = p.Wp + geo.s_off + t * geo.KQ * 256 + 4 * lane;
+    wt[i] = p.Wp + t * geo.KT * TILE_BYTES;
+    ws[i] = p.Wp + geo.s_off + t * geo.KQ * 256;
     rowmax[i] = mx_half(ACT) ? p.Wp[geo.e_off + 16 * t + c] : 0;
   }
   const uint8_t* row[QT];
@@ -55,13 +55,13 @@ __global__ __launch_bounds__(64 * ROW_WAVES) void k_mx_rows(const MxParams p) {
     for (int u = 0; u < QT; ++u) acc[i][u] = f4{0.f, 0.f, 0.f, 0.f};
 
   auto chunk = [&](const uint8_t* r, int k) {          // 16 bytes of a row at element k
-    return *reinterpret_cast<const u4*>(k < p.K ? r + act_bytes<ACT>(k) : mx_zeros);
+    return g_load<u4>(k < p.K ? r + act_bytes<ACT>(k) : mx_zeros);
   };
   auto load = [&](int kt, T& f) {
 #pragma unroll
     for (int i = 0; i < SP; ++i) {
-      f.w[i] = *reinterpret_cast<const u4*>(wt[i] + (int64_t)kt * TILE_BYTES);
-      f.s[i] = ws[i][(kt >> 2) * 256 + (kt & 3)];
+      f.w[i] = g_load<u4>(wt[i] + (int64_t)kt * TILE_BYTES, 16 * lane);
+      f.s[i] = g_load<uint8_t>(ws[i] + (kt >> 2) * 256 + (kt & 3), 4 * lane);
     }
     const int k = 128 * kt;
 #pragma unroll
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES) void k_mx_rows(const MxParams p) {
         f.a[u][0] = chunk(row[u], k + 16 * g), f.a[u][1] = chunk(row[u], k + 64 + 16 * g);
       } else {
         f.a[u][0] = chunk(row[u], k + 32 * g);
-        f.as[u] = *(k + 32 * g < p.K ? srow[u] + 4 * kt + g : mx_zeros);
+        f.as[u] = g_load<uint8_t>(k + 32 * g < p.K ? srow[u] + 4 * kt + g : mx_zeros);
       }
     }
   };
