@@ -2,8 +2,9 @@
 //
 // A (token, choice) is a pair. Two kernels: the first finds each token's experts
 // and writes h = w * act(gate) * up of every pair, the second multiplies by the
-// down projections and sums a token's pairs. Up to ROUTE_IN tokens every block of the
-// first kernel takes the choices itself, above that a kernel before it does.
+// down projections and sums a token's pairs. One token's choices every wave of the
+// first kernel takes itself, more tokens' a kernel before it (which took longer in
+// every block already for two: 33.4 us against 31.0 at 64 experts of 1536).
 //
 // fp16 x meets the weights widened to fp16 (mx_common.hpp). h, a product of two
 // sums, has float32's range: it is kept as two bfloat16 numbers, hi + lo (16 bits
@@ -23,7 +24,6 @@ typedef __bf16 b4v __attribute__((ext_vector_type(4)));
 typedef __bf16 b8v __attribute__((ext_vector_type(8)));
 
 constexpr int MOE_PAIRS = W4_MOE_MAX_TOKENS * W4_MOE_MAX_TOP;
-constexpr int ROUTE_IN = 4;
 constexpr int MOE_COLS = 16;             // tokens that the second kernel takes as columns
 constexpr int MOE_THREADS = 512, MOE_WAVES = 8, ROUTE_THREADS = 1024;
 constexpr int DOWN_SP = 4, DOWN_WAVES = 4;       // strips and waves of a block that takes one expert
@@ -64,14 +64,14 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 
 // One wave: the `top` largest logits of token t (of up to 64 R experts), ties to the
-// lowest expert, and their softmax weights.
+// lowest expert, and their softmax weights, choice j in lane j (-1 for none).
 template <int R>
-__device__ __forceinline__ void route_token(const MoeParams& p, int t, MoeRoute& r, MoeChoice& ch) {
+__device__ __forceinline__ void route_token(const MoeParams& p, int t, int& id, float& weight, bool& bad) {
   const int lane = threadIdx.x & 63;
   const float ninf = -__builtin_inff();
   float v[R];
   uint32_t key[R];
-  bool bad = false;
+  bad = false;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int e = 64 * i + lane;
@@ -83,8 +83,7 @@ __device__ __forceinline__ void route_token(const MoeParams& p, int t, MoeRoute&
     key[i] = e < p.E ? order_key(v[i]) : 0u;
   }
   bad = __ballot(bad) != 0;
-  // lane j keeps choice j
-  int id = -1;
+  id = -1;
   float l = ninf, most = 0.f;
   for (int j = 0; j < p.top; ++j) {
     uint32_t m = 0;
@@ -113,19 +112,14 @@ __device__ __forceinline__ void route_token(const MoeParams& p, int t, MoeRoute&
     for (int i = 0; i < R; ++i) s += v[i] == ninf ? 0.f : expf(v[i] - most);
   }
   s = wave_sum_f(s);
-  if (lane < p.top) {
-    ch.id[t * p.top + lane] = id;
-    r.weight[t * p.top + lane] = id >= 0 ? w / s : -1.f;
-  }
-  if (lane == 0) r.bad[t] = bad;
+  weight = id >= 0 ? w / s : -1.f;
 }
 
 // The whole block: experts in use and their pairs, from the choices. An expert's
 // pairs come in any order: they are columns of its products, none meets another.
-template <int THREADS>
 __device__ __forceinline__ void route_lists(const MoeParams& p, MoeRoute& r, MoeChoice& ch) {
   const int pairs = p.T * p.top, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int i = tid; i < pairs; i += THREADS)
+  for (int i = tid; i < pairs; i += ROUTE_THREADS)
     if (ch.id[i] >= 0) ch.place[i] = atomicAdd(&ch.count[ch.id[i]], 1);
   __syncthreads();
   const int n = tid < p.E ? ch.count[tid] : 0;
@@ -143,7 +137,7 @@ __device__ __forceinline__ void route_lists(const MoeParams& p, MoeRoute& r, Moe
   __syncthreads();
   int a = __builtin_popcountll(used & ((1ull << lane) - 1)), all = 0, sum = 0;
   upto -= n;
-  for (int i = 0; i < THREADS / 64; ++i) {
+  for (int i = 0; i < ROUTE_THREADS / 64; ++i) {
     if (i < wave) a += ch.waves[0][i], upto += ch.waves[1][i];
     all += ch.waves[0][i], sum += ch.waves[1][i];
   }
@@ -156,28 +150,30 @@ __device__ __forceinline__ void route_lists(const MoeParams& p, MoeRoute& r, Moe
   if (tid == 0) r.active = all, r.first[all] = sum;
   const bool columns = p.T <= MOE_COLS;
   if (columns)
-    for (int i = tid; i < all * MOE_COLS / 2; i += THREADS) reinterpret_cast<uint32_t*>(r.column)[i] = 0xFFFFFFFFu;
+    for (int i = tid; i < all * MOE_COLS / 2; i += ROUTE_THREADS) reinterpret_cast<uint32_t*>(r.column)[i] = 0xFFFFFFFFu;
   __syncthreads();
-  for (int i = tid; i < pairs; i += THREADS)
+  for (int i = tid; i < pairs; i += ROUTE_THREADS)
     if (ch.id[i] >= 0) {
       r.list[ch.before[ch.id[i]] + ch.place[i]] = i;
       if (columns) r.column[ch.count[ch.id[i]]][i / p.top] = (int16_t)i;
     }
-  __syncthreads();
-}
-
-template <int R, int THREADS>
-__device__ __forceinline__ void route(const MoeParams& p, MoeRoute& r, MoeChoice& ch) {
-  if (threadIdx.x < W4_MOE_MAX_EXPERTS) ch.count[threadIdx.x] = 0;
-  for (int t = threadIdx.x >> 6; t < p.T; t += THREADS / 64) route_token<R>(p, t, r, ch);
-  __syncthreads();
-  route_lists<THREADS>(p, r, ch);
 }
 
 template <int R>
 __global__ __launch_bounds__(ROUTE_THREADS) void k_moe_route(const MoeParams p) {
   __shared__ MoeChoice ch;
-  route<R, ROUTE_THREADS>(p, *p.route, ch);
+  const int lane = threadIdx.x & 63;
+  if (threadIdx.x < W4_MOE_MAX_EXPERTS) ch.count[threadIdx.x] = 0;
+  for (int t = threadIdx.x >> 6; t < p.T; t += ROUTE_THREADS / 64) {
+    int id;
+    float weight;
+    bool bad;
+    route_token<R>(p, t, id, weight, bad);
+    if (lane < p.top) ch.id[t * p.top + lane] = id, p.route->weight[t * p.top + lane] = weight;
+    if (lane == 0) p.route->bad[t] = bad;
+  }
+  __syncthreads();
+  route_lists(p, *p.route, ch);
 }
 
 __device__ __forceinline__ float moe_act(float g, int act) {
@@ -190,37 +186,54 @@ __device__ __forceinline__ float moe_act(float g, int act) {
 }
 
 // h of P strips of 16 inner rows (gate and up) for one expert's pairs, 16 QT of them at
-// a time. R: the block takes the choices itself (of up to 64 R experts); 0: they are there.
+// a time. R: one token, whose choices (of up to 64 R experts) the waves take themselves;
+// 0: they are there.
 template <int P, int QT, int R, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_moe_up(const MoeParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];     // sums
-  __shared__ typename std::conditional<R != 0, MoeRoute, int>::type own;
-  __shared__ typename std::conditional<R != 0, MoeChoice, int>::type ch;
   constexpr int SP = 2 * P;              // strips: gate, up, gate, up ..
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int strips = p.I / 16, groups = (strips + P - 1) / P;
   const int a = block_number() / groups, s0 = (block_number() - a * groups) * P;
   f4* sums = reinterpret_cast<f4*>(smem);                // [wave][SP][QT][64]
-  // a few tokens' x comes to LDS while the choices are taken, 16 bytes of zeros behind it
-  uint8_t* const xs = smem + WAVES * SP * QT * 1024;
+  uint8_t* const xs = smem + WAVES * SP * QT * 1024;     // the one token's x, 16 bytes of zeros behind it
   const MoeRoute* r = p.route;
-  if constexpr (R != 0) {
-    for (int i = threadIdx.x; i < p.T * p.H / 8; i += 64 * WAVES)
+  int e, n = 1, first = 0, own = 0;
+  float own_weight = 0.f;
+  // (what the weights' addresses come from in scalar registers)
+  if constexpr (R != 0) {                                // every wave for itself
+    for (int i = threadIdx.x; i < p.H / 8; i += 64 * WAVES)
       reinterpret_cast<u4*>(xs)[i] = reinterpret_cast<const u4*>(p.x)[i];
-    if (threadIdx.x == 0) reinterpret_cast<u4*>(xs)[p.T * p.H / 8] = u4{0u, 0u, 0u, 0u};
-    route<R, 64 * WAVES>(p, own, ch);
-    if (block_number() == 0)                             // for the second kernel
-      for (int i = threadIdx.x; i < (int)(sizeof(MoeRoute) / 4); i += 64 * WAVES)
-        reinterpret_cast<int*>(p.route)[i] = reinterpret_cast<const int*>(&own)[i];
-    r = &own;
+    if (threadIdx.x == 0) reinterpret_cast<u4*>(xs)[p.H / 8] = u4{0u, 0u, 0u, 0u};
+    int id;
+    float weight;
+    bool bad;
+    route_token<R>(p, 0, id, weight, bad);
+    const uint64_t chosen = __ballot(id >= 0);
+    const int active = __builtin_popcountll(chosen);
+    int rank = 0;                                        // among the chosen, by expert
+    for (int j = 0; j < active; ++j) rank += __builtin_amdgcn_readlane(id, j) < id;
+    if (block_number() == 0 && wave == 0) {              // for the second kernel
+      MoeRoute& w = *p.route;
+      if (lane < p.top) w.weight[lane] = weight;
+      if (lane < active) w.expert[rank] = id, w.first[rank] = rank, w.list[rank] = lane;
+      if (lane == 0) w.active = active, w.first[active] = active, w.bad[0] = bad;
+      if (lane < active)
+        for (int i = 0; i < MOE_COLS; ++i) w.column[rank][i] = (int16_t)(i == 0 ? lane : -1);
+    }
+    if (a >= active) return;
+    own = __builtin_ctzll(__ballot(id >= 0 && rank == a));
+    e = __builtin_amdgcn_readlane(id, own);
+    own_weight = lane_f(weight, own);
+    __syncthreads();
+  } else {
+    const int active = r->active;
+    e = __builtin_amdgcn_readfirstlane(r->expert[min(a, W4_MOE_MAX_EXPERTS - 1)]);
+    first = __builtin_amdgcn_readfirstlane(r->first[min(a, W4_MOE_MAX_EXPERTS - 1)]);
+    n = __builtin_amdgcn_readfirstlane(r->first[min(a + 1, W4_MOE_MAX_EXPERTS)]) - first;
+    if (a >= active) return;
   }
-  const int active = r->active;
-  // (the weights' addresses in scalar registers)
-  const int e = __builtin_amdgcn_readfirstlane(r->expert[min(a, W4_MOE_MAX_EXPERTS - 1)]);
-  const int first = __builtin_amdgcn_readfirstlane(r->first[min(a, W4_MOE_MAX_EXPERTS - 1)]);
-  const int n = __builtin_amdgcn_readfirstlane(r->first[min(a + 1, W4_MOE_MAX_EXPERTS)]) - first;
-  if (a >= active) return;
   const MxGeometry geo = mx_geometry((int64_t)p.E * 2 * p.I, p.H);
 
   const uint8_t *wt[SP], *ws[SP];
@@ -236,7 +249,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_moe_up(const MoeParams p) {
   for (int n0 = 0; n0 < n; n0 += 16 * QT) {
     int64_t row[QT];                                     // of x
 #pragma unroll
-    for (int u = 0; u < QT; ++u) row[u] = (int64_t)(r->list[first + min(n0 + 16 * u + c, n - 1)] / p.top) * p.H;
+    for (int u = 0; u < QT; ++u)
+      row[u] = R != 0 ? 0 : (int64_t)(r->list[first + min(n0 + 16 * u + c, n - 1)] / p.top) * p.H;
     f4 acc[SP][QT];
 #pragma unroll
     for (int i = 0; i < SP; ++i)
@@ -274,7 +288,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_moe_up(const MoeParams p) {
           for (int u = 0; u < QT; ++u)
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              f[0][u][y] = *reinterpret_cast<const h8*>(xs + 2 * (k < p.H ? (int)row[u] + k + 8 * y : p.T * p.H));
+              f[0][u][y] = *reinterpret_cast<const h8*>(xs + 2 * (k < p.H ? k + 8 * y : p.H));
         }
 #pragma unroll
         for (int i = 0; i < SP; ++i) {
@@ -308,8 +322,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_moe_up(const MoeParams p) {
         for (int y = 0; y < 4; ++y) gv[y] += ga[y], uv[y] += ua[y];
       }
       const uint8_t* top0 = p.w1 + geo.e_off + ((int64_t)e * 2 * strips + s) * 16 + 4 * (l >> 4);
-      const int pair = r->list[first + col];
-      const float weight = r->weight[pair];
+      const int pair = R != 0 ? own : r->list[first + col];
+      const float weight = R != 0 ? own_weight : r->weight[pair];
       b4v hi, lo;
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
@@ -570,8 +584,8 @@ static MoeSpace moe_space(int T, int H, int I, int top) {
 
 template <int P, int QT, int R, int WAVES>
 int launch_up_r(const MoeParams& p, int64_t experts, hipStream_t stream) {
-  const int lds = WAVES * 2 * P * QT * 1024 + (R != 0 ? p.T * p.H * 2 + 16 : 0);
-  allow_smem((const void*)&k_moe_up<P, QT, R, WAVES>, R != 0 ? 100 * 1024 : lds);
+  const int lds = WAVES * 2 * P * QT * 1024 + (R != 0 ? p.H * 2 + 16 : 0);
+  allow_smem((const void*)&k_moe_up<P, QT, R, WAVES>, R != 0 ? 80 * 1024 : lds);
   hipLaunchKernelGGL((k_moe_up<P, QT, R, WAVES>), grid_of(experts * ((p.I / 16 + P - 1) / P)), dim3(64 * WAVES),
                      lds, stream, p);
   return launch_status();
@@ -619,7 +633,7 @@ extern "C" int moe_mx4(const uint16_t* x, const void* logits, int logits_dtype, 
   p.T = tokens, p.H = hidden, p.I = inner, p.E = experts, p.top = top_k, p.act = act;
   p.renorm = renormalize != 0, p.half_logits = logits_dtype == W4_IN_F16;
 
-  const bool in = tokens <= ROUTE_IN && tokens * hidden * 2 <= MOE_X_LDS;
+  const bool in = tokens == 1 && hidden * 2 <= MOE_X_LDS;
   if (!in) {
     if (experts <= 64) hipLaunchKernelGGL(k_moe_route<1>, dim3(1), dim3(ROUTE_THREADS), 0, stream, p);
     else if (experts <= 128) hipLaunchKernelGGL(k_moe_route<2>, dim3(1), dim3(ROUTE_THREADS), 0, stream, p);
