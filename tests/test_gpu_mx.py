@@ -188,6 +188,44 @@ def test_products_at_real_sizes(g, act, M, N, K):
 
 
 @pytest.mark.parametrize("act", ["a16", "a8", "a4"])
+@pytest.mark.parametrize("M,N,K", [(65, 300, 8640), (40, 12500, 2080), (128, 130, 4128)])
+def test_products_split_along_k(g, act, M, N, K):
+    op = {"a16": g.W4_MX_A16, "a8": g.W4_MX_A8, "a4": g.W4_MX_A4}[act]
+    rng = np.random.default_rng(N)
+    codes, scales = weights(rng, N, K)
+    Wp = g.prepack_mx4(dev(codes), dev(scales))
+    w = O.mx4_decode(codes, scales)
+    t, a = rows(rng, act, M, K)
+    need = g.mx4_workspace_bytes(op, M, N, K)
+    assert (need > 16384) == (N < 1000)                  # the wide one has tiles enough
+    raw = torch.zeros(max(need, 256), dtype=torch.uint8, device="cuda")
+    raw[16384:] = 0xFF                                   # only the counters have to be zero
+    for half in (True, False):
+        got = product(g, act)(*t, Wp, N, out_dtype=g.W4_OUT_F16 if half else g.W4_OUT_F32, workspace=raw)
+        check_product(host(got), a, w, None, half, f"{act} {M}x{N}x{K} half {half}")
+        assert not raw[:16384].any()
+    if need:
+        for short in (raw[:need - 1], raw[:16384]):
+            with pytest.raises(g.W4Error):
+                product(g, act)(*t, Wp, N, workspace=short)
+
+
+@pytest.mark.parametrize("M", [7, 70, 300])
+@pytest.mark.parametrize("K", [512, 544])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_a4_scales_at_any_address(g, M, K, off):
+    rng = np.random.default_rng(off)
+    N = 48
+    codes, scales = weights(rng, N, K)
+    t, a = rows(rng, "a4", M, K)
+    s = torch.full((M * K // 32 + off,), 255, dtype=torch.uint8, device="cuda")[off:].view(M, K // 32)
+    s.copy_(t[1])
+    got = g.mx4a4_gemm(t[0], s, g.prepack_mx4(dev(codes), dev(scales)), N, out_dtype=g.W4_OUT_F32,
+                       workspace=g.Workspace())
+    check_product(host(got), a, O.mx4_decode(codes, scales), None, False, "a4")
+
+
+@pytest.mark.parametrize("act", ["a16", "a8", "a4"])
 @pytest.mark.parametrize("M", [3, 100])
 def test_scales_of_any_size(g, act, M):
     """Scales far apart in a row and between rows; float32 out, so nothing overflows."""
@@ -358,6 +396,38 @@ def test_moe(g, T, H, I, E, top):
         m.check(g, *tokens(rng, T, H, E, dt), top, act, renorm, ws, f"T {T} H {H} I {I} E {E} act {act}")
 
 
+@pytest.mark.parametrize("T", [1, 2, 5, 16, 17])
+@pytest.mark.parametrize("H,I,E,top", [(2080, 96, 5, 3), (2048, 32, 140, 6), (2144, 160, 100, 1)])
+def test_moe_wide_hidden(g, T, H, I, E, top):
+    """hidden at which a few tokens are the columns of the second product, and the choices
+    among more than 64 and more than 128 experts."""
+    rng = np.random.default_rng(T + H)
+    m = Layer(g, rng, H, I, E)
+    ws = g.Workspace()
+    for renorm, dt in ((True, np.float32), (False, np.float16)):
+        m.check(g, *tokens(rng, T, H, E, dt), top, 0, renorm, ws, f"T {T} H {H}")
+    x, logits = tokens(rng, T, H, E)
+    logits[-1] = -np.inf
+    assert not host(m.check(g, x, logits, top, ws=ws))[-1].any()
+    logits[-1, E // 2] = np.nan
+    m.check(g, x, logits, top, ws=ws)
+    logits[-1] = 1.0
+    m.check(g, x, logits, top, ws=ws)
+
+
+def test_moe_one_token_longer_than_the_first_product_keeps(g):
+    rng = np.random.default_rng(8)
+    m = Layer(g, rng, 16416, 32, 3)
+    m.check(g, *tokens(rng, 1, 16416, 3), 2)
+
+
+@pytest.mark.parametrize("T", [4, 64])
+def test_moe_most_choices(g, T):
+    rng = np.random.default_rng(9)
+    m = Layer(g, rng, 64, 32, 512)
+    m.check(g, *tokens(rng, T, 64, 512), 16)
+
+
 @pytest.mark.parametrize("T", [5, 40])
 def test_moe_every_token_on_one_expert(g, T):
     rng = np.random.default_rng(1)
@@ -410,19 +480,20 @@ def test_moe_small_and_large_activations(g, T, size, act):
 
 
 @pytest.mark.parametrize("T", [3, 20])
-def test_moe_nan_weights_reach_the_expert_s_tokens_only(g, T):
+@pytest.mark.parametrize("H", [96, 2048])
+def test_moe_nan_weights_reach_the_expert_s_tokens_only(g, T, H):
     rng = np.random.default_rng(5)
-    m = Layer(g, rng, 96, 64, 4)
+    m = Layer(g, rng, H, 64, 4)
     m.s1[2 * 64 * 1 + 5, 1] = 255                        # expert 1, a gate row
-    m.s2[96 * 3 + 7, 1] = 255                            # expert 3, a row of its output
+    m.s2[H * 3 + 7, 1] = 255                             # expert 3, a row of its output
     m.pack(g)
-    x, logits = tokens(rng, T, 96, 4)
+    x, logits = tokens(rng, T, H, 4)
     logits[:, 1] = -9
     logits[0, 1] = 9
     logits[:, 3] = -9
     logits[1, 3] = 9
     y = host(g.moe_mx4(dev(x), dev(logits), 2, m.p1, m.p2, 64, workspace=g.Workspace()))
-    want = np.zeros((T, 96), bool)
+    want = np.zeros((T, H), bool)
     want[0] = True
     want[1, 7] = True
     assert np.array_equal(np.isnan(y), want)
@@ -460,3 +531,61 @@ def test_moe_repeats_on_streams_and_in_graphs(g, T):
         assert torch.equal(out, call(workspace=ws))
     # the workspace serves a product afterwards: its counters are zero
     assert not ws.buf[:16384].any()
+
+
+# ------------------------------------------------------------------ together
+def test_a_step_of_a_layer_in_a_graph(g):
+    """What a decode step runs between its attention and its residual: norm to E4M3 rows, their
+    product, rows to MXFP4, their product, the router's product on fp16 rows, the experts;
+    replayed with other inputs, two streams at once with a workspace each."""
+    rng = np.random.default_rng(21)
+    T, H, I, E, top = 12, 512, 160, 8, 3
+    w = {n: weights(rng, r, H) for n, r in (("a", H), ("b", H), ("r", E))}
+    packed = {n: g.prepack_mx4(dev(c), dev(s)) for n, (c, s) in w.items()}
+    m = Layer(g, rng, H, I, E)
+    gain = (1 + 0.1 * rng.standard_normal(H)).astype(np.float16)
+    dgain = dev(gain)
+
+    def step(x, res, ws):
+        rows, scale, res = g.add_rmsnorm_q8(x, dgain, res, q_dtype=g.W4_Q_F8)
+        y = g.mx4a8_gemm(rows, scale, packed["a"], H, workspace=ws)
+        z = g.mx4a4_gemm(*g.quantize_mx4(y), packed["b"], H, workspace=ws)
+        logits = g.mx4a16_gemm(z, packed["r"], E, out_dtype=g.W4_OUT_F32, workspace=ws)
+        return g.moe_mx4(z, logits, top, m.p1, m.p2, I, workspace=ws), rows, scale, y, z, logits
+
+    xs = [(dev(rng.standard_normal((T, H)).astype(np.float16)), dev(rng.standard_normal((T, H)).astype(np.float16)))
+          for _ in range(3)]
+    eager = [step(x, r, g.Workspace()) for x, r in xs]
+    # each stage against the oracle, on the inputs that it got
+    for out, rows_, scale, y, z, logits in eager:
+        a8 = O.e4m3_decode(host(rows_)).astype(np.float64) * host(scale)[:, None]
+        check_product(host(y), a8, O.mx4_decode(*w["a"]), None, True, "a8")
+        a4 = O.mx4_decode(*O.mx4_encode(host(y)))
+        check_product(host(z), a4, O.mx4_decode(*w["b"]), None, True, "a4")
+        check_product(host(logits), host(z).astype(np.float64), O.mx4_decode(*w["r"]), None, False, "a16")
+        m.check(g, host(z), host(logits), top)
+    graphs = []
+    for x, r in xs[:2]:
+        s, ws = torch.cuda.Stream(), g.Workspace()
+        s.wait_stream(torch.cuda.current_stream())
+        x, r = x.clone(), r.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            step(x, r, ws)                               # allocates the workspace
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                out = step(x, r, ws)[0]
+        graphs.append((graph, s, x, r, out, ws))
+    for i in range(3):
+        for n, (graph, s, x, r, out, _) in enumerate(graphs):
+            x.copy_(xs[(i + n) % 3][0])
+            r.copy_(xs[(i + n) % 3][1])
+        torch.cuda.synchronize()
+        for graph, s, *_ in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for n, (*_, out, ws) in enumerate(graphs):
+            assert torch.equal(out, eager[(i + n) % 3][0])
+            assert not ws.buf[:16384].any()
