@@ -12,7 +12,7 @@
 // bfloat16, with float32 sums.
 //
 // Bound: the bytes of the experts in use. One token on 4 of 64 experts (hidden 4096,
-// inner 1536, 40 MB) takes 11.5 + 7.2 us: choices, one round trip to memory, the weights;
+// inner 1536, 40 MB) takes 9.9 + 7.4 us: choices, one round trip to memory, the weights;
 // 16 tokens on about 41 of them 5 + 57 + 37 us (4.3 TB/s over the two products),
 // 61 tokens on 16 experts (hidden 3200, inner 4320, 352 MB) 7.5 + 54 + 52 us.
 #include "mx_gemm.hpp"
@@ -642,7 +642,8 @@ extern "C" int moe_mx4(const uint16_t* x, const void* logits, int logits_dtype, 
   }
   const int64_t most = min(experts, tokens * top_k);     // experts in use, at most
   // pairs of strips a block where that leaves the CUs enough blocks (that case 57 us, 60
-  // with one; one token on 4 experts 11.5 with one, 13 with two)
+  // with one; one token on 4 experts 11.5 with one, 13 with two, before its choices were
+  // taken without barriers)
   const int st = most * (inner / 16) > 1024 ? launch_up<2>(p, in, most, stream) : launch_up<1>(p, in, most, stream);
   if (st) return st;
   if (moe_columns(tokens, hidden, inner, top_k)) {

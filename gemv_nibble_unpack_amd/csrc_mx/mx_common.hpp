@@ -71,11 +71,12 @@ __device__ __forceinline__ h8 fp4_h8(uint32_t w, float scale) {
 // The fp16 products take a weight as code * 2^(byte - rowmax + H_UP), at most 6 *
 // 2^12 in fp16, and multiply the row's sum by 2^(rowmax - 127 - H_UP): exact
 // for blocks down to 2^-35 of the row's largest scale, below that rounded to
-// 2^-36 of it (fp16's least subnormal).
+// 2^-36 of it (fp16's least subnormal). Blocks of zeros, whose scales rowmax leaves
+// out, may lie above it: held at 2^H_UP, since an exponent of 255 would make them NaN.
 constexpr int H_UP = 12;
 __device__ __forceinline__ float h_scale(uint32_t byte, uint32_t rowmax) {
   const int e = (int)byte - (int)rowmax + 127 + H_UP;
-  return byte == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)max(e, 1) << 23);
+  return byte == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)min(max(e, 1), 127 + H_UP) << 23);
 }
 
 }  // namespace w4

@@ -100,6 +100,8 @@ def _space(key, ask, workspace, device, stream):
         return workspace
     need = _NEED.get(key)
     if need is None:
+        if len(_NEED) > 4096:
+            _NEED.clear()
         need = _NEED[key] = ask(*key[1:])
     return (workspace or Workspace(device)).get(need, stream) if need else None
 

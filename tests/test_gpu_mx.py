@@ -241,6 +241,70 @@ def test_scales_of_any_size(g, act, M):
     check_product(host(got), a, O.mx4_decode(codes, scales), None, False, act)
 
 
+@pytest.mark.parametrize("act", ["a16", "a8", "a4"])
+@pytest.mark.parametrize("M", [3, 100])
+def test_blocks_of_zeros_whatever_their_scale(g, act, M):
+    rng = np.random.default_rng(7)
+    N, K = 20, 256 * 32
+    codes = rng.choice(np.array([0, 8, 128], np.uint8), (N, K // 2))          # +0 and -0
+    scales = np.tile(np.append(np.arange(255), 0), (N, 1)).astype(np.uint8)
+    for n in range(N - 1):                               # one block that is not zeros; the last row has none
+        codes[n, 16 * 255:] = rng.integers(0, 256, 16)
+        scales[n, 255] = 100 + 3 * n
+    Wp = g.prepack_mx4(dev(codes), dev(scales))
+    t, a = rows(rng, act, M, K)
+    for half in (True, False):
+        got = product(g, act)(*t, Wp, N, out_dtype=g.W4_OUT_F16 if half else g.W4_OUT_F32, workspace=g.Workspace())
+        assert torch.isfinite(got[:, N - 1]).all() and not got[:, N - 1].any()
+        if not half:
+            check_product(host(got), a, O.mx4_decode(codes, scales), None, False, act)
+
+
+@pytest.mark.parametrize("M", [2, 66])
+def test_weights_past_4_gib(g, M):
+    """Rows of zeros but for the first and the last strips."""
+    rng = np.random.default_rng(M)
+    N, K, R = (1 << 20) + 5, 8320, 40
+    codes = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(N, K // 32, dtype=torch.uint8, device="cuda")
+    c, s = weights(rng, 2 * R, K)
+    for x, y in ((codes, c), (scales, s)):
+        x[:R] = dev(y[:R])
+        x[N - R:] = dev(y[R:])
+    Wp = g.prepack_mx4(codes, scales)
+    assert Wp.numel() > 1 << 32
+    w = O.mx4_decode(c, s)
+    for act in ("a16", "a8", "a4"):
+        t, a = rows(rng, act, M, K)
+        got = product(g, act)(*t, Wp, N, workspace=g.Workspace())
+        check_product(host(torch.cat((got[:, :R], got[:, N - R:]), 1)), a, w, None, True, act)
+        assert not got[:, R:N - R].any()
+    c2, s2 = g.unprepack_mx4(Wp, N, K)
+    assert torch.equal(c2, codes) and torch.equal(s2, scales)
+
+
+def test_rows_past_4_gib(g):
+    rng = np.random.default_rng(2)
+    M, N, K, R = 262144 + 9, 33, 8320, 300
+    codes, scales = weights(rng, N, K)
+    Wp = g.prepack_mx4(dev(codes), dev(scales))
+    w = O.mx4_decode(codes, scales)
+    x = torch.zeros(M, K, dtype=torch.float16, device="cuda")
+    some = rng.standard_normal((R, K)).astype(np.float16)
+    x[M - R:] = dev(some)
+    got = g.mx4a16_gemm(x, Wp, N, workspace=g.Workspace())
+    check_product(host(got[M - R:]), some.astype(np.float64), w, None, True, "a16")
+    assert not got[:M - R].any()
+    # coded, back, and their product
+    qc, qs = g.quantize_mx4(x)
+    wc, ws_ = O.mx4_encode(some)
+    assert np.array_equal(host(qc[M - R:]), wc) and np.array_equal(host(qs[M - R:]), ws_)
+    back = g.dequantize_mx4(qc, qs)
+    assert np.array_equal(host(back[M - R:]), O.mx4_decode(wc, ws_).astype(np.float16)) and not back[:M - R].any()
+    got = g.mx4a4_gemm(qc, qs, Wp, N, workspace=g.Workspace())
+    check_product(host(got[M - R:]), O.mx4_decode(wc, ws_), w, None, True, "a4")
+
+
 @pytest.mark.parametrize("M", [3, 100])
 def test_a16_blocks_far_below_their_row(g, M):
     """Blocks below 2^-35 of their row's largest scale are rounded to 2^-36 of it."""
@@ -426,6 +490,57 @@ def test_moe_most_choices(g, T):
     rng = np.random.default_rng(9)
     m = Layer(g, rng, 64, 32, 512)
     m.check(g, *tokens(rng, T, 64, 512), 16)
+
+
+@pytest.mark.parametrize("T", [1, 3, 20])
+def test_moe_experts_past_4_gib(g, T):
+    """512 experts of zeros but for the first, one between and the last."""
+    rng = np.random.default_rng(T)
+    H, I, E, used = 8192, 2080, 512, [0, 300, 511]
+
+    def fill(rows, K):
+        c = torch.zeros(E * rows, K // 2, dtype=torch.uint8, device="cuda")
+        s = torch.zeros(E * rows, K // 32, dtype=torch.uint8, device="cuda")
+        hc, hs = weights(rng, len(used) * rows, K)
+        for i, e in enumerate(used):
+            c[e * rows:(e + 1) * rows] = dev(hc[i * rows:(i + 1) * rows])
+            s[e * rows:(e + 1) * rows] = dev(hs[i * rows:(i + 1) * rows])
+        return g.prepack_mx4(c, s), O.mx4_decode(hc, hs).reshape(len(used), rows, K)
+
+    p1, w1 = fill(2 * I, H)
+    p2, w2 = fill(H, I)
+    assert min(p1.numel(), p2.numel()) > 1 << 32
+    m = Layer.__new__(Layer)
+    m.H, m.I, m.E, m.p1, m.p2, m.w1, m.w2 = H, I, E, p1, p2, w1, w2
+    x, few = tokens(rng, T, H, len(used))
+    logits = np.full((T, E), -np.inf, np.float32)
+    logits[:, used] = few
+    got = g.moe_mx4(dev(x), dev(logits), 2, p1, p2, I, workspace=g.Workspace())
+    ref, err = O.moe_layer(x, few, 2, w1, w2, 0, True)
+    tol = err + (2.0 ** -11 + 64 * STEP) * np.abs(ref) + 2.0 ** -25
+    assert np.all(np.abs(host(got).astype(np.float64) - ref) <= tol)
+
+
+@pytest.mark.parametrize("T,H", [(1, 96), (1, 2048), (9, 96), (9, 2048), (40, 160)])
+def test_moe_into_its_input(g, T, H):
+    rng = np.random.default_rng(T)
+    m = Layer(g, rng, H, 64, 4)
+    x, logits = tokens(rng, T, H, 4)
+    want = m.check(g, x, logits, 2)
+    for _ in range(3):
+        y = dev(x)
+        assert g.moe_mx4(y, dev(logits), 2, m.p1, m.p2, 64, workspace=g.Workspace(), out=y) is y
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T", [2, 20])
+def test_moe_rows_of_zeros_whatever_their_scale(g, T):
+    rng = np.random.default_rng(3)
+    m = Layer(g, rng, 8192, 32, 2)
+    m.c1[5] = 0
+    m.s1[5] = np.append(np.arange(255), 116)
+    m.pack(g)
+    m.check(g, *tokens(rng, T, 8192, 2), 2)
 
 
 @pytest.mark.parametrize("T", [5, 40])
