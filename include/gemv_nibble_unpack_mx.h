@@ -56,9 +56,9 @@ int quantize_mx4(const void* X, int in_dtype, int rows, int K, uint8_t* codes, u
                  hipStream_t stream);
 
 /*
- * dequantize_mx4 -- MXFP4 rows to fp16 (W4_OUT_F16; rounded once, infinite past
- * its range) or float32 (W4_OUT_F32; exact) [rows,K], 16-byte aligned. Errors as
- * quantize_mx4.
+ * dequantize_mx4 -- MXFP4 rows to fp16 (W4_OUT_F16; rounded once) or float32
+ * (W4_OUT_F32; exact) [rows,K], 16-byte aligned; infinite past the type's range.
+ * Errors as quantize_mx4.
  */
 int dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int rows, int K, int out_dtype,
                    void* Y, hipStream_t stream);
@@ -97,8 +97,9 @@ int unprepack_mx4(const uint8_t* Wp, int N, int K, uint8_t* codes, uint8_t* scal
  * A block with scale 255 makes every sum that meets it NaN, as a NaN or
  * infinity of A does for its row.
  * Every M is served (M = 0 returns W4_OK without a launch): few rows by a
- * kernel that streams the weights, more by a tiled product. Large buffers 16-byte aligned, a_scale its 4 bytes,
- * a_scales any address. Workspace: mx4_workspace_bytes(op, M, N, K) bytes (0 if
+ * kernel that streams the weights, more by a tiled product (of at most 2^22 tiles;
+ * W4_ERR_SHAPE past that). A, Wp and C are 16-byte aligned, a_scale to 4 bytes, bias to
+ * 2, a_scales lies at any address. The outputs overlap no input. Workspace: mx4_workspace_bytes(op, M, N, K) bytes (0 if
  * none is needed or an argument is invalid), the rules of w4_workspace_bytes.
  * Errors: W4_ERR_ARG (out_dtype), W4_ERR_SHAPE, W4_ERR_NULL, W4_ERR_ALIGN,
  * W4_ERR_WORKSPACE, W4_ERR_HIP.
@@ -126,15 +127,16 @@ int mx4a4_gemm(const uint8_t* Aq, const uint8_t* a_scales, const uint8_t* Wp, co
  *   rows, then its up rows; w_down: of [experts * hidden, inner].
  *   act: W4_ACT_*.
  * Sums are float32 in an order that does not change from call to call. x meets
- * the weights as in mx4a16_gemm; h is float32 and is rounded to fp16
- * for the second product, each 128 inner elements counted from their largest
- * (relative 2^-11 down to 2^-28 of it).
+ * the weights as in mx4a16_gemm; w_j h_j is formed in float32 and kept as the sum of two
+ * bfloat16 numbers for the second product (relative 2^-17), whose weights are
+ * bfloat16 numbers, exact within that type's range.
  * An expert with logit -infinity is never chosen; a token whose logits are all
  * -infinity gets zeros, one that has a NaN or +infinity among them NaN. A NaN in
  * a token's x or in an expert's weights reaches the tokens that meet it.
  *   tokens 0 .. W4_MOE_MAX_TOKENS (0 returns W4_OK without a launch), experts to
  *   W4_MOE_MAX_EXPERTS, top_k to W4_MOE_MAX_TOP and at most experts, hidden and
- *   inner multiples of 32 up to W4_MAX_K. x, weights 16-byte aligned, out 8.
+ *   inner multiples of 32 up to W4_MAX_K. x and weights are 16-byte aligned, out 8;
+ *   out may be x.
  *   Workspace: moe_mx4_workspace_bytes(...) bytes (0 for arguments that are not
  *   served), the rules of w4_workspace_bytes.
  * Errors: W4_ERR_ARG (logits_dtype, act), W4_ERR_SHAPE, W4_ERR_NULL,
