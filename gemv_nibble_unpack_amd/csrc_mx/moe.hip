@@ -46,10 +46,19 @@ struct MoeParams {
   uint16_t* out;
   uint32_t* counters;
   MoeRoute* route;
-  __bf16* h;                             // hi [pairs][I], then lo
+  __bf16* h;                             // [pairs][I], hi, then lo; grouped: see h_at
   float* y;                              // [pairs][H]
-  int T, H, I, E, top, act, renorm, half_logits;
+  int T, H, I, E, top, act, renorm, half_logits, grouped;
 };
+
+// Grouped h: 16 places in `list` by 128 k, in the order in which the second product's
+// lanes take them: hi and lo, four steps of k, then 16 bytes a lane, so that a wave
+// reads whole lines (61 tokens on 16 experts of 4320: 45 us, 53 on rows of h, whose
+// lanes lie a row apart).
+constexpr int H_GROUP = 2 * 16 * 128;
+__host__ __device__ inline int64_t h_group(int place, int kt, int I) {
+  return ((int64_t)(place >> 4) * ((I + 127) / 128) + kt) * H_GROUP;
+}
 
 struct MoeChoice {                       // in LDS while the choices are taken
   int id[MOE_PAIRS];                     // expert, -1 for none
@@ -333,9 +342,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_moe_up(const MoeParams p) {
         const float rest = h - (float)hi[y];
         lo[y] = (__bf16)(abs_bits((float)hi[y]) >= F32_INF ? 0.f : rest);
       }
-      const int64_t at = (int64_t)pair * p.I + 16 * s + 4 * (l >> 4);
+      const int k = 16 * s + 4 * (l >> 4), place = R != 0 ? a : first + col;
+      int64_t at = (int64_t)pair * p.I + k, rest_at = (int64_t)p.T * p.top * p.I;
+      if (p.grouped) {
+        at = h_group(place, k >> 7, p.I) + (k >> 3 & 3) * 512 + ((k >> 5 & 3) * 16 + (place & 15)) * 8 + (k & 4);
+        rest_at = H_GROUP / 2;
+      }
       *reinterpret_cast<u2*>(p.h + at) = __builtin_bit_cast(u2, hi);
-      *reinterpret_cast<u2*>(p.h + (int64_t)p.T * p.top * p.I + at) = __builtin_bit_cast(u2, lo);
+      *reinterpret_cast<u2*>(p.h + at + rest_at) = __builtin_bit_cast(u2, lo);
     }
   }
 }
@@ -468,9 +482,13 @@ __global__ __launch_bounds__(64 * DOWN_WAVES, 4) void k_moe_down_pairs(const Moe
       ws[i] = p.w2 + geo.s_off + ti * geo.KQ * 256;
     }
     const int end = geo.KT * (wave + 1) / WAVES;
-    const int64_t plane = (int64_t)p.T * p.top * p.I;
+    const int kt_step = p.grouped ? H_GROUP : 128, x_step = p.grouped ? 512 : 8;
+    const int lo_step = p.grouped ? H_GROUP / 2 : p.T * p.top * p.I;
     for (int n0 = 0; n0 < n; n0 += 16) {
-      const int pair = n0 + c < n ? r.list[first + n0 + c] : -1;
+      // this lane's h: columns past n take the last one's again, nobody takes theirs
+      const int place = first + min(n0 + c, n - 1);
+      const uint32_t own = p.grouped ? 2 * (uint32_t)(h_group(place, 0, p.I) + (16 * g + (place & 15)) * 8)
+                                     : 2 * (uint32_t)(r.list[place] * p.I + 32 * g);
       f4 acc[SP];
 #pragma unroll
       for (int i = 0; i < SP; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
@@ -488,12 +506,19 @@ __global__ __launch_bounds__(64 * DOWN_WAVES, 4) void k_moe_down_pairs(const Moe
       for (; kt < end; ++kt) {
         HFrag f;
         const int k = 128 * kt + 32 * g;
-        const bool in = pair >= 0 && k < p.I;
-        const __bf16* hp = p.h + (int64_t)pair * p.I + k;
+        const bool in = k < p.I;
+        const uint32_t at = in ? own : 0;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          f.hi[x] = g_load<b8v>(in ? (const uint8_t*)(hp + 8 * x) : mx_zeros);
-          f.lo[x] = g_load<b8v>(in ? (const uint8_t*)(hp + plane + 8 * x) : mx_zeros);
+          f.hi[x] = g_load<b8v>(p.h + (kt * kt_step + x * x_step), at);
+          f.lo[x] = g_load<b8v>(p.h + (kt * kt_step + x * x_step + lo_step), at);
+        }
+        if (128 * kt + 128 > p.I) {                      // the weights there are zeros, h may be a NaN
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            f.hi[x] = in ? f.hi[x] : b8v{};
+            f.lo[x] = in ? f.lo[x] : b8v{};
+          }
         }
         u4 v[SP];
         uint32_t sv[SP];
@@ -528,34 +553,46 @@ __global__ __launch_bounds__(64 * DOWN_WAVES, 4) void k_moe_down_pairs(const Moe
     if (threadIdx.x == 0) dev_store(p.counters + grp, 0u);
   }
   const float nan = __uint_as_float(0x7FC00000u);
-  for (int x = threadIdx.x; x < p.T * SP * 4; x += 64 * WAVES) {
-    const int tok = x / (SP * 4), col = 16 * SP * grp + 4 * (x % (SP * 4));
-    if (col >= p.H) continue;
-    f4 v = {0.f, 0.f, 0.f, 0.f};
-    if (!empty) {
-      // four choices' loads together: each is a round trip to the level that all XCDs share
-      for (int j0 = 0; j0 < p.top; j0 += 4) {
-        uint64_t lo[4], hi[4];
-        float weight[4];
+  // Four pieces of four choices' loads together: each is a round trip to the level that
+  // all XCDs share.
+  constexpr int PIECES = 4, STEP = 64 * WAVES;
+  const int pieces = p.T * SP * 4;
+  for (int x0 = threadIdx.x; x0 < pieces; x0 += PIECES * STEP) {
+    f4 v[PIECES];
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) v[q] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < (empty ? 0 : p.top); j0 += 4) {
+      uint64_t lo[PIECES][4], hi[PIECES][4];
+      float weight[PIECES][4];
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int pr = tok * p.top + min(j0 + j, p.top - 1);
-          const uint32_t* y = reinterpret_cast<const uint32_t*>(p.y) + (int64_t)pr * p.H + col;
-          weight[j] = r.weight[pr];
-          lo[j] = dev_load2(y), hi[j] = dev_load2(y + 2);
+          const int x = x0 + q * STEP, tok = x / (SP * 4), col = 16 * SP * grp + 4 * (x % (SP * 4));
+          weight[q][j] = -1.f;
+          if (x >= pieces || j0 + j >= p.top || col >= p.H) continue;
+          const uint32_t* y = reinterpret_cast<const uint32_t*>(p.y) + (int64_t)(tok * p.top + j0 + j) * p.H + col;
+          weight[q][j] = r.weight[tok * p.top + j0 + j];
+          lo[q][j] = dev_load2(y), hi[q][j] = dev_load2(y + 2);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j0 + j < p.top && weight[j] >= 0.f) {
-            v[0] += __uint_as_float((uint32_t)lo[j]), v[1] += __uint_as_float((uint32_t)(lo[j] >> 32));
-            v[2] += __uint_as_float((uint32_t)hi[j]), v[3] += __uint_as_float((uint32_t)(hi[j] >> 32));
-          }
-      }
-    }
-    h4 o;
+      for (int q = 0; q < PIECES; ++q)
 #pragma unroll
-    for (int y = 0; y < 4; ++y) o[y] = (_Float16)(r.bad[tok] ? nan : v[y]);
-    *reinterpret_cast<u2*>(p.out + (int64_t)tok * p.H + col) = __builtin_bit_cast(u2, o);
+        for (int j = 0; j < 4; ++j)
+          if (weight[q][j] >= 0.f) {
+            v[q][0] += __uint_as_float((uint32_t)lo[q][j]), v[q][1] += __uint_as_float((uint32_t)(lo[q][j] >> 32));
+            v[q][2] += __uint_as_float((uint32_t)hi[q][j]), v[q][3] += __uint_as_float((uint32_t)(hi[q][j] >> 32));
+          }
+    }
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      const int x = x0 + q * STEP, tok = x / (SP * 4), col = 16 * SP * grp + 4 * (x % (SP * 4));
+      if (x >= pieces || col >= p.H) continue;
+      h4 o;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) o[y] = (_Float16)(r.bad[tok] ? nan : v[q][y]);
+      *reinterpret_cast<u2*>(p.out + (int64_t)tok * p.H + col) = __builtin_bit_cast(u2, o);
+    }
   }
 }
 
@@ -571,13 +608,19 @@ static bool moe_columns(int T, int H, int I, int top) {
   return T <= MOE_COLS && H >= 128 * 16 && (int64_t)T * top * I * 4 <= MOE_H_LDS;
 }
 
+// h grouped: where an expert has more than 4 pairs in the mean (16 tokens on 64 experts of
+// 1536, one pair each: 37 us in rows, 40 grouped; 61 on 16 of 4320: 53 and 45)
+static bool moe_grouped(int T, int H, int I, int E, int top) {
+  return !moe_columns(T, H, I, top) && T * top > 4 * E;
+}
+
 struct MoeSpace {
   int64_t h, y, total;
 };
-static MoeSpace moe_space(int T, int H, int I, int top) {
+static MoeSpace moe_space(int T, int H, int I, int E, int top) {
   MoeSpace s;
   s.h = WS_COUNTERS + (int64_t)((sizeof(MoeRoute) + 255) / 256 * 256);
-  s.y = s.h + (int64_t)T * top * I * 4;
+  s.y = s.h + (moe_grouped(T, H, I, E, top) ? h_group(T * top + 15, 0, I) * 2 : (int64_t)T * top * I * 4);
   s.total = s.y + (moe_columns(T, H, I, top) ? 0 : (int64_t)T * top * H * 4);
   return s;
 }
@@ -608,7 +651,7 @@ using namespace w4;
 
 extern "C" size_t moe_mx4_workspace_bytes(int tokens, int hidden, int inner, int experts, int top_k) {
   if (!moe_sizes_ok(tokens, hidden, inner, experts, top_k) || tokens == 0) return 0;
-  return (size_t)moe_space(tokens, hidden, inner, top_k).total;
+  return (size_t)moe_space(tokens, hidden, inner, experts, top_k).total;
 }
 
 extern "C" int moe_mx4(const uint16_t* x, const void* logits, int logits_dtype, int tokens, int hidden,
@@ -623,7 +666,7 @@ extern "C" int moe_mx4(const uint16_t* x, const void* logits, int logits_dtype, 
   if (!aligned(x, 16) || !aligned(logits, logits_dtype == W4_IN_F16 ? 2 : 4) ||
       !aligned(w_gate_up, 16) || !aligned(w_down, 16) || !aligned(out, 8) || !aligned(workspace, 256))
     return W4_ERR_ALIGN;
-  const MoeSpace s = moe_space(tokens, hidden, inner, top_k);
+  const MoeSpace s = moe_space(tokens, hidden, inner, experts, top_k);
   if (!workspace || workspace_bytes < (size_t)s.total) return W4_ERR_WORKSPACE;
   uint8_t* ws = (uint8_t*)workspace;
   MoeParams p{};
@@ -631,6 +674,7 @@ extern "C" int moe_mx4(const uint16_t* x, const void* logits, int logits_dtype, 
   p.counters = (uint32_t*)ws, p.route = (MoeRoute*)(ws + WS_COUNTERS);
   p.h = (__bf16*)(ws + s.h), p.y = (float*)(ws + s.y);
   p.T = tokens, p.H = hidden, p.I = inner, p.E = experts, p.top = top_k, p.act = act;
+  p.grouped = moe_grouped(tokens, hidden, inner, experts, top_k);
   p.renorm = renormalize != 0, p.half_logits = logits_dtype == W4_IN_F16;
 
   const bool in = tokens == 1 && hidden * 2 <= MOE_X_LDS;
