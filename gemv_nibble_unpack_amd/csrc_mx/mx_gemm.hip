@@ -77,7 +77,7 @@ __device__ __forceinline__ void mx_gemm_tile(const MxParams& p, int mblocks, int
   const int wm = wave % S::WM, wn = wave / S::WM;
   const int l31 = lane & 31, half = lane >> 5;
   const int r = lane & 15, hi = (lane >> 4) & 1;         // this lane's weight row: strip 2 j + hi, row r
-  const int m0 = mb * S::BM, t0 = nb * S::STRIPS;
+  const int m0 = mb * S::BM, t0 = p.strip0 + nb * S::STRIPS;
   const int KB = p.K / 32;
   // this block's k tiles: whole quads
   const int kt0 = 4 * (int)((int64_t)geo.KQ * split / splits);
@@ -435,6 +435,7 @@ struct MxPlan {
   int bm, bn, splits;
   int64_t tiles;
   size_t ws;
+  int first;                             // columns of a first launch of 256 x 256 tiles
 };
 static MxPlan mx_plan(int act, int M, int N, int K) {
   // The tile by the most that a CU gets of it, in units of a 256 x 256 tile's time
@@ -445,16 +446,28 @@ static MxPlan mx_plan(int act, int M, int N, int K) {
   const int bms[4] = {256, 128, 128, 64}, bns[4] = {256, 256, 128, 128}, each[4] = {100, 60, 34, 22};
   MxPlan best{};
   int64_t least = INT64_MAX;
-  for (int x = act == W4_MX_A16; x < 4; ++x) {
-    const int64_t tiles = (int64_t)ceil_div(M, bms[x]) * ceil_div(N, bns[x]);
-    const int64_t cost = (tiles + 255) / 256 * each[x];
-    if (cost < least) least = cost, best = MxPlan{bms[x], bns[x], 1, tiles, 0};
+  auto consider = [&](int first, int64_t before) {       // of the columns from `first` on
+    for (int x = act == W4_MX_A16; x < 4; ++x) {
+      const int64_t tiles = (int64_t)ceil_div(M, bms[x]) * ceil_div(N - first, bns[x]);
+      const int64_t cost = before + (tiles + 255) / 256 * each[x];
+      if (cost < least) least = cost, best = MxPlan{bms[x], bns[x], 1, tiles, 0, first};
+    }
+  };
+  consider(0, 0);
+  // Whole rounds of 256 x 256 tiles, then the other columns in the tile that is best
+  // for them, a second launch (4): 2048 x 11008 x 4096 97 -> 91 us on 8-bit rows and 80 -> 76
+  // on 4-bit ones, 2048 x 12288 x 4096 99 -> 94 and 82 -> 78. No such split of fp16 rows'
+  // largest tile gains by this count.
+  const int64_t rows = ceil_div(M, 256), rounds = rows * ceil_div(N, 256) / 256;
+  if (act != W4_MX_A16 && rounds > 0) {
+    const int64_t columns = 256 * (rounds * 256 / rows);
+    if (columns > 0 && columns < N) consider((int)columns, rounds * each[0] + 4);
   }
   // The smallest tile where it leaves CUs without work: splits along k, of whole quads
   // of k tiles. A k tile takes 0.55, 0.3 or 0.26 us (fp16, 8-bit, 4-bit rows), the
   // exchange about 3 us and 0.017 for each block: 45 x 3200 x 8640, 8-bit rows, 26 us
   // whole, 14.7 in 4, 15.3 in 8; 200 x 4096 x 4096, fp16, 30 whole, 25 in 2 or 4.
-  if (best.bm == 64 && best.tiles < 256) {
+  if (best.bm == 64 && best.tiles < 256 && best.first == 0) {
     const int KT = (K + 127) / 128, KQ = (KT + 3) / 4;
     const double t = act == W4_MX_A16 ? 0.55 : act == W4_MX_A8 ? 0.3 : 0.26;
     double least_us = t * KT;
@@ -469,12 +482,13 @@ static MxPlan mx_plan(int act, int M, int N, int K) {
 
 template <int ACT, typename S>
 int launch_tile(const MxParams& p, const MxPlan& plan, hipStream_t stream) {
+  // (the columns from p.strip0 on)
   const int64_t blocks = plan.tiles * plan.splits;
   if (blocks > (1 << 22)) return W4_ERR_SHAPE;
   const int per_xcd = (int)((blocks + 7) / 8);
   allow_smem((const void*)&k_mx_gemm<ACT, S>, S::LDS);
   hipLaunchKernelGGL((k_mx_gemm<ACT, S>), dim3(per_xcd * 8), dim3(S::THREADS), S::LDS, stream, p,
-                     ceil_div(p.M, S::BM), ceil_div(p.N, S::BN), per_xcd, plan.splits);
+                     ceil_div(p.M, S::BM), (int)(plan.tiles / ceil_div(p.M, S::BM)), per_xcd, plan.splits);
   return launch_status();
 }
 
@@ -483,7 +497,7 @@ int launch_tile(const MxParams& p, const MxPlan& plan, hipStream_t stream) {
 // 42), which hide the widening of the weights, 8-bit and 4-bit rows four (2048 x
 // 8192 x 4096 67 and 50 us, 93 and 52 on eight).
 template <int ACT, int RS>
-int launch_gemm(const MxParams& p, hipStream_t stream) {
+int launch_gemm(MxParams p, hipStream_t stream) {
   const MxPlan plan = mx_plan(ACT == MX_A8_EXACT ? W4_MX_A8 : ACT, p.M, p.N, p.K);
   if constexpr (ACT == W4_MX_A16) {
     if (plan.bn == 256) return launch_tile<ACT, MxTile<ACT, 2, 4, 2, 2, 3, RS>>(p, plan, stream);
@@ -491,6 +505,11 @@ int launch_gemm(const MxParams& p, hipStream_t stream) {
     return launch_tile<ACT, MxTile<ACT, 2, 4, 1, 1, 3, RS>>(p, plan, stream);
   } else {
     constexpr int NS = ACT == W4_MX_A4 ? 4 : 3;
+    if (plan.first > 0) {
+      const MxPlan whole{256, 256, 1, (int64_t)ceil_div(p.M, 256) * (plan.first / 256), 0, 0};
+      if (const int st = launch_tile<ACT, MxTile<ACT, 2, 2, 4, 4, NS, RS>>(p, whole, stream)) return st;
+      p.strip0 = plan.first / 16;
+    }
     if (plan.bm == 256) return launch_tile<ACT, MxTile<ACT, 2, 2, 4, 4, NS, RS>>(p, plan, stream);
     if (plan.bn == 256) return launch_tile<ACT, MxTile<ACT, 2, 2, 2, 4, 4, RS>>(p, plan, stream);
     if (plan.bm == 128) return launch_tile<ACT, MxTile<ACT, 2, 2, 2, 2, NS, RS>>(p, plan, stream);

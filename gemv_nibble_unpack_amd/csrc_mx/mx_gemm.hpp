@@ -15,6 +15,7 @@ struct MxParams {
   uint32_t* counters;        // split sums: arrivals per output tile
   float* part;               // and partial sums
   int M, N, K, out;
+  int strip0;                // tiled products: the first of the launch's strips
 };
 
 // E4M3 rows through fp16 products. The matrix cores' 8-bit products drop, in

@@ -210,6 +210,24 @@ def test_products_split_along_k(g, act, M, N, K):
                 product(g, act)(*t, Wp, N, workspace=short)
 
 
+@pytest.mark.parametrize("act", ["a8", "a4"])
+@pytest.mark.parametrize("M,N,K", [(1000, 17001, 160), (1000, 20011, 96), (2000, 9000, 160), (2048, 11008, 64)])
+def test_products_in_two_launches(g, act, M, N, K):
+    """Sizes whose whole rounds of large tiles leave columns for smaller ones."""
+    rng = np.random.default_rng(N)
+    codes, scales = weights(rng, N, K)
+    Wp = g.prepack_mx4(dev(codes), dev(scales))
+    w = O.mx4_decode(codes, scales)
+    t, a = rows(rng, act, M, K)
+    bias = rng.standard_normal(N).astype(np.float16)
+    for half in (True, False):
+        guard = torch.full((M * N + 64,), 7.0, dtype=torch.float16 if half else torch.float32, device="cuda")
+        got = product(g, act)(*t, Wp, N, bias=dev(bias), out_dtype=g.W4_OUT_F16 if half else g.W4_OUT_F32,
+                              C=guard[:M * N].view(M, N))
+        check_product(host(got), a, w, bias.astype(np.float64), half, f"{act} {M}x{N}x{K} half {half}")
+        assert (guard[M * N:] == 7).all()
+
+
 @pytest.mark.parametrize("M", [7, 70, 300])
 @pytest.mark.parametrize("K", [512, 544])
 @pytest.mark.parametrize("off", [1, 2, 3])
