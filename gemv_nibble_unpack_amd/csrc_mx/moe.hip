@@ -14,7 +14,7 @@
 // Bound: the bytes of the experts in use. One token on 4 of 64 experts (hidden 4096,
 // inner 1536, 40 MB) takes 9.9 + 7.4 us: choices, one round trip to memory, the weights;
 // 16 tokens on about 41 of them 5 + 57 + 37 us (4.3 TB/s over the two products),
-// 61 tokens on 16 experts (hidden 3200, inner 4320, 352 MB) 7.5 + 54 + 52 us.
+// 61 tokens on 16 experts (hidden 3200, inner 4320, 352 MB) 7.5 + 54 + 44 us.
 #include "mx_gemm.hpp"
 
 namespace w4 {
@@ -455,8 +455,8 @@ __global__ __launch_bounds__(MOE_THREADS) void k_moe_down_tokens(const MoeParams
 // SP strips of one expert for its pairs, 16 of them at a time; the last block of a
 // group of strips sums each token's pairs, in the order of its choices.
 // Four blocks of four waves a CU (128 registers), a k tile's weights on their way while the one
-// before is multiplied. us at 16 tokens on 64 experts of 1536 and 61 on 16 of 4320: 37.3
-// and 52, eight waves 45.7 and 49; two strips a block 46 and 60.
+// before is multiplied. us at 16 tokens on 64 experts of 1536 and 61 on 16 of 4320, with rows
+// of h: 37.3 and 52, eight waves 45.7 and 49; two strips a block 46 and 60; now 38 and 44.
 __global__ __launch_bounds__(64 * DOWN_WAVES, 4) void k_moe_down_pairs(const MoeParams p) {
   constexpr int SP = DOWN_SP, WAVES = DOWN_WAVES;
   __shared__ f4 sums[WAVES][SP][64];

@@ -11,7 +11,7 @@
 // Bound: the matrix cores and what they draw. Instructions alone, on random data, reach 4.2
 // PFLOP/s (4-bit weights, 8-bit rows), 6.8 (4-bit rows) and 1.7 (fp16); zeros a third
 // more. A call of 2048 x 4096 x 11008, 8-bit rows, takes 76 us (2.4 PFLOP/s), 2048 x 11008 x
-// 4096 77 on 4-bit rows (2.4) and 185 on fp16 rows (1.0), 777 x 4096 x 4096 on fp16 rows
+// 4096 73 on 4-bit rows (2.5) and 185 on fp16 rows (1.0), 777 x 4096 x 4096 on fp16 rows
 // 34. A 256 x 256 tile's stage of 4-bit rows takes 0.93 to 1.07 us: its matrix
 // instructions 0.70, its loads, which a loop without waits or on one hot stage does
 // not shorten, the rest.

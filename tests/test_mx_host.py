@@ -92,6 +92,14 @@ def test_product_refusals(act):
     assert call(**{f"_{5 + o}": 0, "_0": None}) == L.W4_OK
 
 
+@pytest.mark.parametrize("act", ["a16", "a8", "a4"])
+def test_products_of_too_many_tiles(act):
+    s = [] if act == "a16" else [P]
+    for M, N in ((1 << 30, 1 << 30), (1 << 30, 4096), (300, 1 << 30)):
+        st = getattr(G.load(), f"mx4{act}_gemm")(P, *s, P, None, P, 0, M, N, 32, None, 0, None)
+        assert st == L.W4_ERR_SHAPE and G.mx4_workspace_bytes(int(act == "a8") + 2 * (act == "a4"), M, N, 32) == 0
+
+
 #      x  logits dt T  H   I   E  k  ren act w1 w2 out ws nb stream
 MOE = [P, P, 1, 3, 64, 96, 8, 2, 1, 0, P, P, P, P, 1 << 30, None]
 
