@@ -449,7 +449,7 @@ class Layer:
 
     def check(self, g, x, logits, top, act=0, renorm=True, ws=None, what=""):
         got = g.moe_mx4(dev(x), dev(logits), top, self.p1, self.p2, self.I, act=act, renormalize=renorm,
-                        workspace=ws or g.Workspace())
+                        workspace=g.Workspace() if ws is None else ws)
         ref, err = O.moe_layer(x, logits, top, self.w1, self.w2, act, renorm)
         y = host(got).astype(np.float64)
         nan = np.isnan(ref)
@@ -501,6 +501,23 @@ def test_moe_one_token_longer_than_the_first_product_keeps(g):
     rng = np.random.default_rng(8)
     m = Layer(g, rng, 16416, 32, 3)
     m.check(g, *tokens(rng, 1, 16416, 3), 2)
+
+
+@pytest.mark.parametrize("T", [1, 6, 16, 40, 64])
+@pytest.mark.parametrize("H,I,E,top", [(96, 160, 4, 3), (2048, 96, 4, 3), (160, 224, 16, 16), (64, 96, 60, 2)])
+def test_moe_on_a_workspace_of_nan(g, T, H, I, E, top):
+    """Only the counters have to be zero; some choices are none, and exactly the bytes asked for are there."""
+    rng = np.random.default_rng(T + E)
+    m = Layer(g, rng, H, I, E)
+    x, logits = tokens(rng, T, H, E)
+    logits[rng.random((T, E)) < 0.5] = -np.inf
+    need = g.moe_mx4_workspace_bytes(T, H, I, E, top)
+    raw = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+    raw[:16384] = 0
+    m.check(g, x, logits, top, ws=raw[:need])
+    assert not raw[:16384].any() and (raw[need:] == 255).all()
+    with pytest.raises(g.W4Error):
+        m.check(g, x, logits, top, ws=raw[:need - 1])
 
 
 @pytest.mark.parametrize("T", [4, 64])
