@@ -187,7 +187,7 @@ __global__ __launch_bounds__(ROUTE_THREADS) void k_moe_route(const MoeParams p) 
 
 __device__ __forceinline__ float moe_act(float g, int act) {
   if (act == W4_ACT_RELU2) {
-    g = fmaxf(g, 0.f);
+    g = g < 0.f ? 0.f : g;               // (a maximum would lose a NaN)
     return g * g;
   }
   const float z = act == W4_ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
