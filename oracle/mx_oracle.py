@@ -112,7 +112,9 @@ def moe_layer(x, logits, top, w1, w2, act, renorm):
             z = np.abs(g) if act == 0 else 0 * g if act == 2 else 1.6 * (np.abs(g) + 0.045 * np.abs(g) ** 3)
             own = (16 + 4 * np.minimum(z, 100.0)) * U * np.abs(f)
             dh = np.abs(u) * (slope * dg + own) + np.abs(f) * du + dg * slope * du + 4 * U * np.abs(h)
-            dh = dh + 2.0 ** -11 * np.abs(h) + 2.0 ** -38 * np.abs(h).max(initial=0.0)   # fp16
+            # two bfloat16 numbers: the first leaves at most half a step of 8 bits, 2^(e - 8) for h of
+            # [2^e, 2^(e+1)), and of that the second at most half a step, 2^(e - 17)
+            dh = dh + 2.0 ** -17 * np.abs(h)
             a = np.abs(w2[e])
             out[t] += p * (w2[e] @ h)
             err[t] += p * (a @ dh + (I / 16 + 64) * U * (a @ np.abs(h)))
