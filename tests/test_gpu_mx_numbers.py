@@ -117,3 +117,53 @@ def test_8_bit_rows_of_normal_data(g, M, N, K):  # noqa: F811
     err = np.linalg.norm(got[0].astype(np.float64) - (ref + bias.astype(np.float64))) / np.linalg.norm(ref)
     assert err <= 8e-6 + (K / 16 + 16) * STEP + 2.0 ** -21, err
     print(f"{err:.3g} of the norm", flush=True)
+
+
+# ------------------------------------------------------------------ far from one
+@pytest.mark.parametrize("M", [3, 40, 100])
+@pytest.mark.parametrize("low,up", [(-24, 14), (-24, -3), (-20, 0)])
+def test_fp16_rows_of_subnormal_numbers(g, M, low, up):  # noqa: F811
+    """Rows of whole multiples of 2^low, results down to fp16's subnormals: the sum rounded once."""
+    rng = np.random.default_rng(M)
+    N, K = 70, 544
+    codes, scales, w = exact_weights(rng, N, K)
+    a = rng.integers(-4, 5, (M, K)).astype(np.float64) * 2.0 ** low
+    t = dev(a.astype(np.float16))
+    assert np.array_equal(host(t).astype(np.float64), a)
+    Wp = g.prepack_mx4(dev(codes), dev((scales.astype(int) + up).astype(np.uint8)))
+    want = a @ w.T * 2.0 ** up
+    for half in (True, False):
+        got = host(g.mx4a16_gemm(t, Wp, N, out_dtype=g.W4_OUT_F16 if half else g.W4_OUT_F32, workspace=g.Workspace()))
+        assert np.array_equal(got, want.astype(np.float16 if half else np.float32)), half
+
+
+@pytest.mark.parametrize("M", [3, 40, 100])
+@pytest.mark.parametrize("low,up", [(-127, 120), (-126, 126), (-107, 100), (-60, 40), (60, -70), (110, -115)])
+def test_8_bit_rows_far_from_one(g, M, low, up):  # noqa: F811
+    """Weights and the rows' scale far apart; E4M3's least numbers, of which 2^-9 is one unit."""
+    rng = np.random.default_rng(M)
+    N, K = 70, 544
+    codes, scales, w = exact_weights(rng, N, K)
+    a = rng.integers(-7, 8, (M, K)) / 512.0
+    f8 = torch.from_numpy(a).to(torch.float8_e4m3fn)
+    assert torch.equal(f8.double(), torch.from_numpy(a))
+    Wp = g.prepack_mx4(dev(codes), dev((scales.astype(int) + low).astype(np.uint8)))
+    want = a @ w.T * 2.0 ** (low + up)
+    for half in (True, False):
+        got = host(g.mx4a8_gemm(f8.cuda(), dev(np.full(M, 2.0 ** up, np.float32)), Wp, N, workspace=g.Workspace(),
+                                out_dtype=g.W4_OUT_F16 if half else g.W4_OUT_F32))
+        assert np.array_equal(got, want.astype(np.float16 if half else np.float32)), (half, got[0, :4], want[0, :4])
+
+
+@pytest.mark.parametrize("M", [3, 40, 100])
+@pytest.mark.parametrize("low,up", [(-127, 127), (127, -127), (-100, 95), (-60, -60), (80, 30)])
+def test_4_bit_rows_far_from_one(g, M, low, up):  # noqa: F811
+    rng = np.random.default_rng(M)
+    N, K = 70, 544
+    codes, scales, w = exact_weights(rng, N, K)
+    ca, sa, a = exact_weights(rng, M, K)
+    Wp = g.prepack_mx4(dev(codes), dev((scales.astype(int) + low).astype(np.uint8)))
+    want = a @ w.T * 2.0 ** (low + up)
+    got = host(g.mx4a4_gemm(dev(ca), dev((sa.astype(int) + up).astype(np.uint8)), Wp, N, out_dtype=g.W4_OUT_F32,
+                            workspace=g.Workspace()))
+    assert np.array_equal(got, want.astype(np.float32)), (got[0, :4], want[0, :4])
