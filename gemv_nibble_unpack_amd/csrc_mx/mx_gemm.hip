@@ -8,13 +8,18 @@
 // so a lane ends with runs of four columns of C. Rows, weights and scales come to
 // LDS by direct loads, a ring of NS stages of 128 k.
 //
-// Bound: the matrix cores and what they draw. Instructions alone, on random data, reach 4.2
-// PFLOP/s (4-bit weights, 8-bit rows), 6.8 (4-bit rows) and 1.7 (fp16); zeros a third
-// more. A call of 2048 x 4096 x 11008, 8-bit rows, takes 76 us (2.4 PFLOP/s), 2048 x 11008 x
-// 4096 73 on 4-bit rows (2.5) and 185 on fp16 rows (1.0), 777 x 4096 x 4096 on fp16 rows
-// 34. A 256 x 256 tile's stage of 4-bit rows takes 0.93 to 1.07 us: its matrix
-// instructions 0.70, its loads, which a loop without waits or on one hot stage does
-// not shorten, the rest.
+// Instructions alone, on random data, reach 4.2 PFLOP/s (4-bit weights, 8-bit rows), 6.8 (4-bit
+// rows) and 1.7 (fp16); zeros a third more. A call of 2048 x 4096 x 11008, 8-bit rows, takes 75 us
+// (2.5 PFLOP/s), 2048 x 11008 x 4096 72 on 4-bit rows (2.6) and 185 on fp16 rows (1.0), 777 x
+// 4096 x 4096 on fp16 rows 35.
+//
+// Bound: the loop's matrix instructions, then its loads, then what is outside it. A stage of 128 k in
+// us, whole, with all loads on one stage that the caches hold, without loads, without loads and LDS
+// reads, instructions at the rates above: 8-bit rows, 128 x 256 tile, 0.78, 0.68, 0.62, 0.59, 0.51; 4-bit rows, 256 x
+// 256, 1.06, 1.00, 0.79, 0.71, 0.63; fp16 rows, 128 x 256, 1.82, 1.71, 1.53, 1.41, 1.26. So a stage's loads
+// cost their issue and their way into LDS, and with 8-bit rows more what comes from behind the
+// caches (221 MB for 46 of operands). Launch, first loads and the result are 11 us (8-bit rows,
+// 2048 x 4096 of them) and 15 (4-bit rows, 2048 x 8192).
 #include "mx_gemm.hpp"
 
 namespace w4 {
@@ -439,10 +444,13 @@ struct MxPlan {
 };
 static MxPlan mx_plan(int act, int M, int N, int K) {
   // The tile by the most that a CU gets of it, in units of a 256 x 256 tile's time
-  // (100). 8-bit rows, us, 256 x 256, 128 x 256, 128 x 128, 64 x 128: 2048 x 8192 x
-  // 4096 76, 83, 80, 105; 2048 x 4096 x 11008 116, 84, 91, 124; 777 x 4096 x 4096
-  // 44, 28, 21.5, 21.0; 200 x 4096 x 4096 43, 25, 19, 14.5. fp16 rows have no 256 x
-  // 256 tile, whose stages would not fit.
+  // (100). us, 256 x 256, 128 x 256, 128 x 128, 64 x 128, of 8-bit rows; of 4-bit rows; of fp16
+  // rows, which have no 256 x 256 tile, since its stages would not fit:
+  //   2048 x 8192 x 4096   60, 71, 74, 115;   48, 55, 74, 95;    133, 174, 194
+  //   2048 x 4096 x 11008  118, 79, 88, 126;  86, 63, 84, 103;   170, 195, 238
+  //   777 x 4096 x 4096    47, 29, 22, 22;    36, 24, 19, 21;    56, 37, 42
+  //   200 x 4096 x 4096    44, 26, 19, 14.5;  33, 22, 17, 13;    47, 29, 23
+  // The units choose the least of each (777 8-bit rows: 22.0, where the last takes 21.7).
   const int bms[4] = {256, 128, 128, 64}, bns[4] = {256, 256, 128, 128}, each[4] = {100, 60, 34, 22};
   MxPlan best{};
   int64_t least = INT64_MAX;

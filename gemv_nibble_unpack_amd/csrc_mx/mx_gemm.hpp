@@ -23,7 +23,8 @@ struct MxParams {
 // adding 2^8 and 2^-6 on the instruction; fp4 x fp4 is exact, fp16 sums are float32):
 // 8e-6 of the norm of normal data, at worst 2^-10 of the sum of magnitudes.
 // That is below the rounding of an fp16 result on data that is not made for it;
-// a float32 result is summed from fp16 products, at a third of the rate.
+// a float32 result is summed from fp16 products (us of a call: 2048 x 4096 x 11008 151 where
+// fp16 takes 80, 777 x 4096 x 4096 36 and 21, 45 x 3200 x 8640 13.8 and 12.2).
 constexpr int MX_A8_EXACT = 3;
 constexpr bool mx_row8(int act) { return act == W4_MX_A8 || act == MX_A8_EXACT; }
 constexpr bool mx_half(int act) { return act == W4_MX_A16 || act == MX_A8_EXACT; }

@@ -5,10 +5,12 @@
 // the caches, 16 a column operand. D = W A^T: a lane ends with four
 // neighbouring columns of C for one row. The waves' sums meet in LDS.
 //
-// Bound: the weights' bytes, and for one short matrix launch and two round trips to
-// memory. us: 1 x 4096 x 4096 fp16 4.6 (9 MB; 1.8 at the copy rate), 27 x 11008 x 4096
-// fp16 13.4 (24 MB, 5.0), 45 x 3200 x 8640 8-bit rows 12.9 (200 blocks on 256 CUs), 8 x
-// 4096 x 11008 4-bit rows 7.6 (24 MB, 5.0).
+// Bound: round trips to memory, a few one after another in each wave (waits are 47 to 72%
+// of the waves' lives, the matrix cores 2 to 9% busy), and with many rows what each block reads
+// of them. us: 1 x 4096 x 4096 fp16 4.6 (9 MB; 1.8 at the copy rate), 27 x 11008 x 4096 fp16 13.7
+// (24 MB, 5.1; a block reads 221 KB of rows beside 104 of weights), 45 x 3200 x 8640 8-bit rows
+// 13.0 (15 MB, 3.1; 389 KB beside 73, 200 blocks on 256 CUs), 8 x 4096 x 11008 4-bit rows
+// 7.5 (24 MB, 5.0).
 #include "mx_gemm.hpp"
 
 namespace w4 {
@@ -185,8 +187,9 @@ int launch_rows_sp(const MxParams& p, hipStream_t stream) {
 
 // Strips a block: rounds of blocks over the 256 CUs times what a block reads for a k
 // tile, SP KiB of weights and the rows. N = 11008, K = 4096, us for 1, 2, 3, 4 strips:
-// 27 fp16 rows 24.0, 18.7, 12.1, 13.4, one 4-bit row 5.0, 6.2, 4.9, 5.7; N = 4096: 16
-// 8-bit rows 4.9, 5.8, 6.3, 7.1.
+// 27 fp16 rows 26.3, 20.9, 14.6, 17.3, 64 8-bit rows 28.3, 20.8, 13.9, 15.3, one 4-bit row 6.5, 8.1,
+// 6.8, 7.5; N = 4096: 16 8-bit rows 5.6, 7.4, 7.8, 9.1. Where one round of three strips and two
+// of two are near each other it can be off: one fp16 row, N = 11008, 10.2, 8.8, 9.6, 11.8.
 template <int ACT, int QT>
 int launch_rows(const MxParams& p, hipStream_t stream) {
   const int strips = ceil_div(p.N, 16);

@@ -83,19 +83,20 @@ int unprepack_mx4(const uint8_t* Wp, int N, int K, uint8_t* codes, uint8_t* scal
  * weights (Wp from prepack_mx4) and float32 sums:
  *   mx4a16_gemm: A fp16 [M,K];
  *   mx4a8_gemm:  Aq E4M3 codes [M,K], a_scale float32 [M]: an element is code *
- *                a_scale (what add_rmsnorm_q8 with W4_Q_F8 and quantize_f8 write);
+ *                a_scale (what add_rmsnorm_q8 with W4_Q_F8 and quantize_f8 write); the
+ *                sum of code * W is a float32 number, which a_scale multiplies;
  *   mx4a4_gemm:  Aq, a_scales MXFP4 rows, uint8 [M,K/2] and [M,K/32].
  *   W4_OUT_F16: C = fp16(sum + bias[n]), bias fp16 [N] or NULL; W4_OUT_F32: C = sum
  *   (bias ignored). Other out_dtypes are refused.
  * 4-bit rows meet the weights in the matrix cores' own scaled products (exact
- * terms, float32 sums), and so do 8-bit rows for an fp16 result: there, terms below
- * 2^-13 of the largest of eight neighbours along k are dropped (8e-6 of the
- * result's norm on normal data, at worst 2^-10 of the sum of magnitudes). For a float32
- * result 8-bit rows, and fp16 rows always, meet weights that are widened to fp16,
- * counted from row n's largest scale: exact for blocks whose scale is at least 2^-35 of the
+ * terms, float32 sums), and so do 8-bit rows for an fp16 result: there, the bits
+ * of terms below 2^-13 of the largest of eight neighbours along k are dropped (8e-6 of the
+ * result's norm on normal data, at worst 2^-10 of the sum of magnitudes; where that is
+ * too much, W4_OUT_F32 keeps them). For a float32 result 8-bit rows, and fp16 rows
+ * always, meet weights that are widened to fp16, counted from row n's largest scale: exact for blocks whose scale is at least 2^-35 of the
  * largest in their row of W, rounded to 2^-36 of the largest below that.
- * A block with scale 255 makes every sum that meets it NaN, as a NaN or
- * infinity of A does for its row.
+ * A block with scale 255 makes every sum that meets it NaN, as a NaN of A does for
+ * its row, which an infinity makes infinite or NaN.
  * Every M is served (M = 0 returns W4_OK without a launch): few rows by a
  * kernel that streams the weights, more by a tiled product (of at most 2^22 tiles;
  * W4_ERR_SHAPE past that). A, Wp and C are 16-byte aligned, a_scale to 4 bytes, bias to
