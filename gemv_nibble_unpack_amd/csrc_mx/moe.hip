@@ -12,8 +12,8 @@
 // bfloat16, with float32 sums.
 //
 // Bound: the bytes of the experts in use. One token on 4 of 64 experts (hidden 4096,
-// inner 1536, 40 MB) takes 9.9 + 7.4 us: choices, one round trip to memory, the weights;
-// 16 tokens on about 41 of them 5 + 57 + 37 us (4.3 TB/s over the two products),
+// inner 1536, 40 MB) takes 10.1 + 7.7 us: choices, one round trip to memory, the weights;
+// 16 tokens on about 41 of them 5 + 57 + 39 us (4.3 TB/s over the two products),
 // 61 tokens on 16 experts (hidden 3200, inner 4320, 352 MB) 7.5 + 54 + 44 us.
 #include "mx_gemm.hpp"
 
